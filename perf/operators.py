@@ -311,7 +311,7 @@ def _marshal(s):
         return sp.prepare_attn_decode(dims, s["q"], *pools, s["table"], s["offs"], s["ctx_len"], s["q_len"], s["cls"],
                                       s["scale"], s["o"], s["lse"], s["workspace"])
     if c["op"] == "write":
-        return sp.prepare_build_q8(dims, s["k"], s["v"], s["cu_k"], s["q_len"], s["cls"], s["table"], s["offs"], None, *pools)
+        return sp.prepare_build_quant(dims, s["k"], s["v"], s["cu_k"], s["q_len"], s["cls"], s["table"], s["offs"], None, *pools)
     if c["op"] == "append":
         return sp.prepare_append(dims, s["k_new"], s["v_new"], s["cu_new"], s["ctx_len"], s["q_len"], s["cls"], s["table"],
                                  s["offs"], *pools)
