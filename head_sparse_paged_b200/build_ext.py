@@ -7,10 +7,10 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsegpaged.so")
-SOURCES = ["segpaged_api.cu", "segpaged_mass.cu"]
+SOURCES = ["segpaged_api.cu", "segpaged_mass.cu", "segpaged_decode.cu"]
 HEADERS = ["sm100_ptx.cuh", "plan.h", "host_common.h", "rope.cuh", "build_kernel.cuh", "prefill_sm100.cuh", "combine_kernel.cuh",
-           "mass_sm100.cuh", "topk_kernel.cuh"]
-NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
+           "mass_sm100.cuh", "topk_kernel.cuh", "quant_rows.cuh", "quant_pages.cuh", "decode_sm100.cuh"]
+NVCC_FLAGS = ["-t", "0", "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
               "-Xcompiler", "-fPIC", "-shared"]
 
 

@@ -40,6 +40,7 @@ const char* segpaged_error_string(int code) {
     case SEGPAGED_ERR_CUDA: return "a CUDA runtime or driver call failed";
     case SEGPAGED_ERR_ALIGN: return "a base pointer is not 16-byte aligned";
     case SEGPAGED_ERR_UNSUPPORTED: return "the plan splits units; this entry point needs a plan made with split_ctas = 0";
+    case SEGPAGED_ERR_FORMAT: return "a pool format this call does not take";
     default: return "unknown error";
   }
 }

@@ -1,0 +1,247 @@
+// segpaged_decode.cu -- host side of the decode-side calls (see include/segpaged.h): the 8-bit build, the append
+// of new rows, the read back, and single-token attention. Argument checks and launches; allocates no device memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/segpaged.h"
+#include "decode_sm100.cuh"
+#include "host_common.h"
+#include "plan.h"
+#include "quant_pages.cuh"
+
+using namespace segpaged;
+using namespace segpaged::host;
+
+static_assert(kFmtBf16 == SEGPAGED_KV_BF16 && kFmtE4m3 == SEGPAGED_KV_E4M3 && kFmtInt8 == SEGPAGED_KV_INT8, "pool formats");
+
+namespace {
+
+bool is_8bit(int32_t fmt) { return fmt == SEGPAGED_KV_E4M3 || fmt == SEGPAGED_KV_INT8; }
+
+// The checks every call here shares: dims, the pool format, the pools and their exponent bytes.
+int check_pools(const segpaged_dims* dims, int32_t fmt, bool allow_bf16, const void* k_pool, const void* v_pool,
+                const uint8_t* kv_scale) {
+  const int rc = check_dims(dims);
+  if (rc) return rc;
+  if (!is_8bit(fmt) && !(allow_bf16 && fmt == SEGPAGED_KV_BF16)) return SEGPAGED_ERR_FORMAT;
+  if ((int64_t)dims->num_seqs * dims->num_q_heads > INT32_MAX) return SEGPAGED_ERR_DIMS;
+  if (dims->num_seqs == 0) return SEGPAGED_OK;
+  if (!k_pool || !v_pool || (is_8bit(fmt) && !kv_scale)) return SEGPAGED_ERR_NULL;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || (is_8bit(fmt) && !aligned16(kv_scale))) return SEGPAGED_ERR_ALIGN;
+  if (dims->num_pages < 1) return SEGPAGED_ERR_DIMS;
+  return SEGPAGED_OK;
+}
+
+int sm_count() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return device_sm_count(dev);
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA; }
+
+template <int D, int FMT>
+void launch_build_quant(const BuildQuantParams& p, int grid, cudaStream_t st) {
+  if (p.b.cos_sin) build_quant_kernel<D, FMT, true><<<grid, 256, 0, st>>>(p);
+  else build_quant_kernel<D, FMT, false><<<grid, 256, 0, st>>>(p);
+}
+
+template <int D, int FMT>
+void launch_append(const AppendParams& p, cudaStream_t st) {
+  const int64_t lanes = (int64_t)p.total_new * p.Hkv * (D / 16);
+  append_kernel<D, FMT><<<(unsigned)ceil_div(lanes, 128), 128, 0, st>>>(p);
+}
+
+template <int D, int FMT>
+int launch_decode(const DecodeParams& p, cudaStream_t st) {
+  const int64_t warps = (int64_t)p.B * p.Hkv * p.G;
+  decode_kernel<D, FMT><<<(unsigned)ceil_div(warps, 4), 128, 0, st>>>(p);
+  return launched();
+}
+
+}  // namespace
+
+// FN<D, FMT>(args) for the call's head_dim and pool format.
+#define SEGPAGED_BY_SHAPE(FN, ...)                                            \
+  do {                                                                        \
+    if (dims->head_dim == 128) {                                              \
+      if (kv_format == SEGPAGED_KV_E4M3) FN<128, kFmtE4m3> __VA_ARGS__;       \
+      else if (kv_format == SEGPAGED_KV_INT8) FN<128, kFmtInt8> __VA_ARGS__;  \
+      else FN<128, kFmtBf16> __VA_ARGS__;                                     \
+    } else {                                                                  \
+      if (kv_format == SEGPAGED_KV_E4M3) FN<64, kFmtE4m3> __VA_ARGS__;        \
+      else if (kv_format == SEGPAGED_KV_INT8) FN<64, kFmtInt8> __VA_ARGS__;   \
+      else FN<64, kFmtBf16> __VA_ARGS__;                                      \
+    }                                                                         \
+  } while (0)
+// The same for the calls that take 8-bit pools only.
+#define SEGPAGED_BY_SHAPE_8BIT(FN, ...)                                 \
+  do {                                                                  \
+    if (dims->head_dim == 128) {                                        \
+      if (kv_format == SEGPAGED_KV_E4M3) FN<128, kFmtE4m3> __VA_ARGS__; \
+      else FN<128, kFmtInt8> __VA_ARGS__;                               \
+    } else {                                                            \
+      if (kv_format == SEGPAGED_KV_E4M3) FN<64, kFmtE4m3> __VA_ARGS__;  \
+      else FN<64, kFmtInt8> __VA_ARGS__;                                \
+    }                                                                   \
+  } while (0)
+
+extern "C" int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format, const void* k_dense, const void* v_dense,
+                                 const int32_t* cu_seqlens_k, const int32_t* q_len, const segpaged_head_class* cls,
+                                 const int32_t* page_table, const int32_t* page_table_offs, const float* rope_cos_sin,
+                                 void* k_pool, void* v_pool, uint8_t* kv_scale, int32_t* status, void* stream) {
+  const int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
+  if (rc) return rc;
+  if (dims->num_seqs == 0) return SEGPAGED_OK;
+  if (!k_dense || !v_dense || !cu_seqlens_k || !q_len || !cls || !page_table || !page_table_offs) return SEGPAGED_ERR_NULL;
+  if (!aligned16(k_dense) || !aligned16(v_dense) || (rope_cos_sin && !aligned16(rope_cos_sin))) return SEGPAGED_ERR_ALIGN;
+  const int sms = sm_count();
+  if (sms <= 0) return SEGPAGED_ERR_CUDA;
+  BuildQuantParams p;
+  p.b.k_dense = static_cast<const __nv_bfloat16*>(k_dense);
+  p.b.v_dense = static_cast<const __nv_bfloat16*>(v_dense);
+  p.b.cu_k = cu_seqlens_k;
+  p.b.q_len = q_len;
+  p.b.cls = reinterpret_cast<const int32_t*>(cls);
+  p.b.table = page_table;
+  p.b.offs = page_table_offs;
+  p.b.cos_sin = rope_cos_sin;
+  p.b.k_pool = nullptr;
+  p.b.v_pool = nullptr;
+  p.b.status = status;
+  p.b.B = dims->num_seqs;
+  p.b.Hkv = dims->num_kv_heads;
+  p.b.P = dims->page_size;
+  p.b.num_pages = dims->num_pages;
+  p.k_pool = static_cast<uint8_t*>(k_pool);
+  p.v_pool = static_cast<uint8_t*>(v_pool);
+  p.kv_scale = kv_scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SEGPAGED_BY_SHAPE_8BIT(launch_build_quant, (p, sms * 8, st));
+  return launched();
+}
+
+extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, const void* k_new, const void* v_new,
+                               int32_t total_new, const int32_t* cu_seqlens_new, const int32_t* ctx_len,
+                               const int32_t* q_len, const segpaged_head_class* cls, const int32_t* page_table,
+                               int64_t page_table_len, const int32_t* page_table_offs, void* k_pool, void* v_pool,
+                               uint8_t* kv_scale, int32_t* status, void* stream) {
+  const int rc = check_pools(dims, kv_format, true, k_pool, v_pool, kv_scale);
+  if (rc) return rc;
+  if (total_new < 0 || page_table_len < 0) return SEGPAGED_ERR_DIMS;
+  if (dims->num_seqs == 0 || total_new == 0) return SEGPAGED_OK;
+  if (!k_new || !v_new || !cu_seqlens_new || !ctx_len || !cls || (!page_table && page_table_len > 0) || !page_table_offs) return SEGPAGED_ERR_NULL;
+  if (!aligned16(k_new) || !aligned16(v_new)) return SEGPAGED_ERR_ALIGN;
+  if (ceil_div((int64_t)total_new * dims->num_kv_heads * (dims->head_dim / 16), 128) > INT32_MAX) return SEGPAGED_ERR_DIMS;
+  AppendParams p;
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.cu_new = cu_seqlens_new;
+  p.ctx_len = ctx_len;
+  p.q_len = q_len;
+  p.cls = reinterpret_cast<const int32_t*>(cls);
+  p.table = page_table;
+  p.offs = page_table_offs;
+  p.k_pool = static_cast<uint8_t*>(k_pool);
+  p.v_pool = static_cast<uint8_t*>(v_pool);
+  p.kv_scale = kv_scale;
+  p.status = status;
+  p.table_len = page_table_len;
+  p.total_new = total_new;
+  p.B = dims->num_seqs;
+  p.Hkv = dims->num_kv_heads;
+  p.P = dims->page_size;
+  p.num_pages = dims->num_pages;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SEGPAGED_BY_SHAPE(launch_append, (p, st));
+  return launched();
+}
+
+namespace {
+template <int D, int FMT>
+void launch_dequant(const DequantParams& p, int grid, cudaStream_t st) {
+  dequant_pages_kernel<D, FMT><<<grid, 256, 0, st>>>(p);
+}
+}  // namespace
+
+extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_format, const int32_t* ctx_len,
+                                      const int32_t* q_len, const segpaged_head_class* cls, const int32_t* page_table,
+                                      int64_t page_table_len, const int32_t* page_table_offs, const void* k_pool,
+                                      const void* v_pool, const uint8_t* kv_scale, void* k_out, void* v_out,
+                                      int32_t* status, void* stream) {
+  const int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
+  if (rc) return rc;
+  if (page_table_len < 0) return SEGPAGED_ERR_DIMS;
+  if (dims->num_seqs == 0) return SEGPAGED_OK;
+  if (!ctx_len || !cls || (!page_table && page_table_len > 0) || !page_table_offs || !k_out || !v_out) return SEGPAGED_ERR_NULL;
+  if (!aligned16(k_out) || !aligned16(v_out)) return SEGPAGED_ERR_ALIGN;
+  const int sms = sm_count();
+  if (sms <= 0) return SEGPAGED_ERR_CUDA;
+  DequantParams p;
+  p.ctx_len = ctx_len;
+  p.q_len = q_len;
+  p.cls = reinterpret_cast<const int32_t*>(cls);
+  p.table = page_table;
+  p.offs = page_table_offs;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.kv_scale = kv_scale;
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.status = status;
+  p.table_len = page_table_len;
+  p.B = dims->num_seqs;
+  p.Hkv = dims->num_kv_heads;
+  p.P = dims->page_size;
+  p.num_pages = dims->num_pages;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SEGPAGED_BY_SHAPE_8BIT(launch_dequant, (p, sms * 8, st));
+  return launched();
+}
+
+extern "C" size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims) {
+  (void)dims;
+  return 256;
+}
+
+extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format, const void* q, const void* k_pool,
+                                    const void* v_pool, const uint8_t* kv_scale, const int32_t* page_table,
+                                    int64_t page_table_len, const int32_t* page_table_offs, const int32_t* ctx_len,
+                                    const int32_t* q_len, const segpaged_head_class* cls, float softmax_scale, void* o,
+                                    float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                                    void* stream) {
+  int rc = check_pools(dims, kv_format, true, k_pool, v_pool, kv_scale);
+  if (rc) return rc;
+  if (page_table_len < 0) return SEGPAGED_ERR_DIMS;
+  if (dims->num_seqs == 0) return SEGPAGED_OK;
+  if (!q || (!page_table && page_table_len > 0) || !page_table_offs || !ctx_len || !cls || !o || !lse || !workspace) return SEGPAGED_ERR_NULL;
+  if (workspace_bytes < segpaged_decode_workspace_bytes(dims)) return SEGPAGED_ERR_CAPACITY;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return SEGPAGED_ERR_ALIGN;
+  DecodeParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.kv_scale = kv_scale;
+  p.table = page_table;
+  p.offs = page_table_offs;
+  p.ctx_len = ctx_len;
+  p.q_len = q_len;
+  p.cls = reinterpret_cast<const int32_t*>(cls);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.status = status;
+  p.table_len = page_table_len;
+  p.B = dims->num_seqs;
+  p.Hkv = dims->num_kv_heads;
+  p.G = dims->num_q_heads / dims->num_kv_heads;
+  p.P = dims->page_size;
+  p.num_pages = dims->num_pages;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = SEGPAGED_OK;
+  SEGPAGED_BY_SHAPE(rc = launch_decode, (p, st));
+  return rc;
+}

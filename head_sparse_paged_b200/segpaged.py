@@ -28,7 +28,8 @@ EXPORTS = ("segpaged_error_string", "segpaged_pages_bytes", "segpaged_rope_cos_s
            "segpaged_prefill_plan", "segpaged_prefill_workspace_bytes", "segpaged_attn_prefill",
            "segpaged_attn_prefill_rope", "segpaged_rope_realign", "segpaged_prefill_plan_append", "segpaged_attn_prefill_append",
            "segpaged_attn_prefill_noalloc", "segpaged_mass_plan", "segpaged_mass_workspace_bytes",
-           "segpaged_token_mass", "segpaged_select_topk")
+           "segpaged_token_mass", "segpaged_select_topk", "segpaged_build_quant", "segpaged_append", "segpaged_pages_dequant",
+           "segpaged_decode_workspace_bytes", "segpaged_attn_decode")
 
 
 class SegPagedError(RuntimeError):
@@ -108,6 +109,17 @@ def _load():
                                         ctypes.c_size_t, vp, vp]
     lib.segpaged_select_topk.restype = ctypes.c_int
     lib.segpaged_select_topk.argtypes = [i32, vp, vp, vp, vp, vp]
+    lib.segpaged_build_quant.restype = ctypes.c_int
+    lib.segpaged_build_quant.argtypes = [dp, i32] + [vp] * 13
+    lib.segpaged_append.restype = ctypes.c_int
+    lib.segpaged_append.argtypes = [dp, i32, vp, vp, i32, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    lib.segpaged_pages_dequant.restype = ctypes.c_int
+    lib.segpaged_pages_dequant.argtypes = [dp, i32, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.segpaged_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.segpaged_decode_workspace_bytes.argtypes = [dp]
+    lib.segpaged_attn_decode.restype = ctypes.c_int
+    lib.segpaged_attn_decode.argtypes = [dp, i32, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp,
+                                         ctypes.c_size_t, vp, vp]
     return lib
 
 
@@ -398,3 +410,150 @@ def segpaged_select_topk(mass, cu_seqlens_q, k_per_seq, selected, stream=None):
                                   _stream(stream))
     if r < 0:
         raise SegPagedError(r, "segpaged_select_topk")
+
+
+KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
+_KV_FORMATS = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
+
+
+def kv_format(pool: torch.Tensor) -> int:
+    """The format a pool's dtype stands for: bfloat16, float8_e4m3fn or int8."""
+    if pool.dtype not in _KV_FORMATS:
+        raise ValueError(f"k_pool: expected bfloat16, float8_e4m3fn or int8, got {pool.dtype}")
+    return _KV_FORMATS[pool.dtype]
+
+
+def _size(t: torch.Tensor | None, n: int, what: str):
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{what}: expected at least {n} elements, got {t.numel()}")
+
+
+def _pools(dims: Dims, k_pool, v_pool, kv_scale):
+    """(format, K pool, V pool, exponent bytes) of a decode-side call, checked against each other and dims."""
+    fmt = kv_format(k_pool)
+    rows = dims.num_pages * dims.page_size
+    _size(k_pool, rows * dims.head_dim, "k_pool")
+    _size(v_pool, rows * dims.head_dim, "v_pool")
+    if fmt == KV_BF16:
+        kv_scale = None
+    elif kv_scale is None:
+        raise ValueError(f"kv_scale: a {k_pool.dtype} pool needs its exponent bytes")
+    _size(kv_scale, 2 * rows, "kv_scale")
+    return fmt, _dev(k_pool, None, "k_pool"), _dev(v_pool, k_pool.dtype, "v_pool"), _dev(kv_scale, torch.uint8, "kv_scale")
+
+
+def _seq_args(dims: Dims, ctx_len, q_len, cls, page_table, page_table_offs):
+    """(ctx_len, q_len, cls, page_table, its length, page_table_offs) of a decode-side call."""
+    B, BH = dims.num_seqs, dims.num_seqs * dims.num_kv_heads
+    _size(ctx_len, B, "ctx_len")
+    _size(q_len, B, "q_len")
+    _size(cls, 3 * BH, "cls")
+    _size(page_table_offs, BH + 1, "page_table_offs")
+    return (_dev(ctx_len, torch.int32, "ctx_len"), _dev(q_len, torch.int32, "q_len"), _dev(cls, torch.int32, "cls"),
+            _dev(page_table, torch.int32, "page_table"), int(page_table.numel()),
+            _dev(page_table_offs, torch.int32, "page_table_offs"))
+
+
+def prepare_build_quant(dims: Dims, k_dense, v_dense, cu_seqlens_k, q_len, cls, page_table, page_table_offs, rope_cos_sin,
+                     k_pool, v_pool, kv_scale, status=None) -> PreparedCall:
+    """segpaged_build_quant with its arguments checked and marshalled once (see PreparedCall)."""
+    bf = torch.bfloat16
+    d = dims.c()
+    fmt, kp, vp, ks = _pools(dims, k_pool, v_pool, kv_scale)
+    args = (ctypes.byref(d), fmt, _dev(k_dense, bf, "k_dense"), _dev(v_dense, bf, "v_dense"),
+            _dev(cu_seqlens_k, torch.int32, "cu_seqlens_k"), _dev(q_len, torch.int32, "q_len"),
+            _dev(cls, torch.int32, "cls"), _dev(page_table, torch.int32, "page_table"),
+            _dev(page_table_offs, torch.int32, "page_table_offs"), _dev(rope_cos_sin, torch.float32, "rope_cos_sin"),
+            kp, vp, ks, _dev(status, torch.int32, "status"))
+    return PreparedCall(_lib.segpaged_build_quant, "segpaged_build_quant", args,
+                        (d, k_dense, v_dense, cu_seqlens_k, q_len, cls, page_table, page_table_offs, rope_cos_sin, k_pool,
+                         v_pool, kv_scale, status))
+
+
+def segpaged_build_quant(dims: Dims, k_dense, v_dense, cu_seqlens_k, q_len, cls, page_table, page_table_offs, rope_cos_sin,
+                      k_pool, v_pool, kv_scale, status=None, stream=None):
+    """segpaged_build into float8_e4m3fn or int8 pools [num_pages, P, D] with exponent bytes kv_scale
+    [num_pages, 2, P] uint8 (K rows, then V rows); the pools' dtype picks the format."""
+    prepare_build_quant(dims, k_dense, v_dense, cu_seqlens_k, q_len, cls, page_table, page_table_offs, rope_cos_sin, k_pool,
+                     v_pool, kv_scale, status)(stream)
+
+
+def prepare_append(dims: Dims, k_new, v_new, cu_seqlens_new, ctx_len, q_len, cls, page_table, page_table_offs, k_pool,
+                   v_pool, kv_scale, status=None) -> PreparedCall:
+    """segpaged_append with its arguments checked and marshalled once (see PreparedCall)."""
+    bf = torch.bfloat16
+    d = dims.c()
+    fmt, kp, vp, ks = _pools(dims, k_pool, v_pool, kv_scale)
+    L, ql, c, tab, n, offs = _seq_args(dims, ctx_len, q_len, cls, page_table, page_table_offs)
+    _size(v_new, k_new.numel(), "v_new")
+    _size(cu_seqlens_new, dims.num_seqs + 1, "cu_seqlens_new")
+    if k_new.shape[1:] != (dims.num_kv_heads, dims.head_dim):
+        raise ValueError(f"k_new: expected [rows, {dims.num_kv_heads}, {dims.head_dim}], got {tuple(k_new.shape)}")
+    args = (ctypes.byref(d), fmt, _dev(k_new, bf, "k_new"), _dev(v_new, bf, "v_new"), int(k_new.shape[0]),
+            _dev(cu_seqlens_new, torch.int32, "cu_seqlens_new"), L, ql, c, tab, n, offs, kp, vp, ks,
+            _dev(status, torch.int32, "status"))
+    return PreparedCall(_lib.segpaged_append, "segpaged_append", args,
+                        (d, k_new, v_new, cu_seqlens_new, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool,
+                         kv_scale, status))
+
+
+def segpaged_append(dims: Dims, k_new, v_new, cu_seqlens_new, ctx_len, q_len, cls, page_table, page_table_offs, k_pool,
+                    v_pool, kv_scale, status=None, stream=None):
+    """The new tokens' K/V rows [total_new, Hkv, D] bf16 into their pages: rows [cu[b], cu[b+1]) are the last tokens
+    of sequence b, whose length ctx_len counts them. Quantised for an 8-bit pool, copied for a bf16 one (kv_scale
+    None). q_len None: tables laid out for one query row."""
+    prepare_append(dims, k_new, v_new, cu_seqlens_new, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool,
+                   kv_scale, status)(stream)
+
+
+def prepare_pages_dequant(dims: Dims, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool, kv_scale, k_out,
+                          v_out, status=None) -> PreparedCall:
+    """segpaged_pages_dequant with its arguments checked and marshalled once (see PreparedCall)."""
+    bf = torch.bfloat16
+    d = dims.c()
+    fmt, kp, vp, ks = _pools(dims, k_pool, v_pool, kv_scale)
+    n_out = dims.num_pages * dims.page_size * dims.head_dim
+    _size(k_out, n_out, "k_out")
+    _size(v_out, n_out, "v_out")
+    args = (ctypes.byref(d), fmt, *_seq_args(dims, ctx_len, q_len, cls, page_table, page_table_offs), kp, vp, ks,
+            _dev(k_out, bf, "k_out"), _dev(v_out, bf, "v_out"), _dev(status, torch.int32, "status"))
+    return PreparedCall(_lib.segpaged_pages_dequant, "segpaged_pages_dequant", args,
+                        (d, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool, kv_scale, k_out, v_out,
+                         status))
+
+
+def segpaged_pages_dequant(dims: Dims, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool, kv_scale, k_out,
+                           v_out, status=None, stream=None):
+    """Every stored page of 8-bit pools read back into bf16 pools of the same page ids."""
+    prepare_pages_dequant(dims, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool, kv_scale, k_out, v_out,
+                          status)(stream)
+
+
+def segpaged_decode_workspace_bytes(dims: Dims) -> int:
+    return int(_lib.segpaged_decode_workspace_bytes(ctypes.byref(dims.c())))
+
+
+def prepare_attn_decode(dims: Dims, q, k_pool, v_pool, kv_scale, page_table, page_table_offs, ctx_len, q_len, cls,
+                        softmax_scale, o, lse, workspace, status=None) -> PreparedCall:
+    """segpaged_attn_decode with its arguments checked and marshalled once (see PreparedCall)."""
+    bf = torch.bfloat16
+    d = dims.c()
+    fmt, kp, vp, ks = _pools(dims, k_pool, v_pool, kv_scale)
+    L, ql, c, tab, n, offs = _seq_args(dims, ctx_len, q_len, cls, page_table, page_table_offs)
+    rows = dims.num_seqs * dims.num_q_heads
+    for t, need, what in ((q, rows * dims.head_dim, "q"), (o, rows * dims.head_dim, "o"), (lse, rows, "lse")):
+        _size(t, need, what)
+    args = (ctypes.byref(d), fmt, _dev(q, bf, "q"), kp, vp, ks, tab, n, offs, L, ql, c, float(softmax_scale),
+            _dev(o, bf, "o"), _dev(lse, torch.float32, "lse"), _dev(workspace, None, "workspace"),
+            int(workspace.numel() * workspace.element_size()), _dev(status, torch.int32, "status"))
+    return PreparedCall(_lib.segpaged_attn_decode, "segpaged_attn_decode", args,
+                        (d, q, k_pool, v_pool, kv_scale, page_table, page_table_offs, ctx_len, q_len, cls, o, lse,
+                         workspace, status))
+
+
+def segpaged_attn_decode(dims: Dims, q, k_pool, v_pool, kv_scale, page_table, page_table_offs, ctx_len, q_len, cls,
+                         softmax_scale, o, lse, workspace, status=None, stream=None):
+    """One new token per sequence: O [B, Hq, D] bf16 and LSE [Hq, B] float32, written in place, of q [B, Hq, D] at
+    position ctx_len - 1 over bf16, float8_e4m3fn or int8 pools (kv_scale None for bf16)."""
+    prepare_attn_decode(dims, q, k_pool, v_pool, kv_scale, page_table, page_table_offs, ctx_len, q_len, cls, softmax_scale,
+                        o, lse, workspace, status)(stream)

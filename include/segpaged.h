@@ -61,6 +61,13 @@ extern "C" {
 #define SEGPAGED_ERR_ALIGN (-8)     /* a base pointer is not 16-byte aligned */
 #define SEGPAGED_ERR_UNSUPPORTED (-9) /* the plan splits units, which this entry point does not accept */
 
+#define SEGPAGED_ERR_FORMAT (-10)   /* a pool format this call does not take */
+
+/* Element formats of a pool (the decode-side calls; the prefill-side calls take bf16 pools). */
+#define SEGPAGED_KV_BF16 0
+#define SEGPAGED_KV_E4M3 1  /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 */
+#define SEGPAGED_KV_INT8 2  /* codes -127 .. 127 */
+
 #define SEGPAGED_STATUS_PAGE_ID 1   /* a page id was outside [0, num_pages); it was clamped */
 #define SEGPAGED_STATUS_TABLE 2     /* a head's page-table length disagreed with the storage rule */
 #define SEGPAGED_STATUS_TIMEOUT 4   /* a pipeline wait gave up; outputs of this call are undefined */
@@ -366,6 +373,88 @@ int segpaged_token_mass(const segpaged_dims* dims, const void* q, int32_t total_
  */
 int segpaged_select_topk(int32_t num_seqs, const float* mass, const int32_t* cu_seqlens_q, const int32_t* k_per_seq,
                          int32_t* selected, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Decode: one new token per sequence against the stored pages, and 8-bit pools.
+ *
+ * Lengths and classes are read from device memory, and nothing is planned on the host, so a captured
+ * call can be replayed while the lengths, tables and classes in those arrays change. In all calls below
+ *   ctx_len (dev) [B]: L_b, the new tokens included (a negative value counts as 0);
+ *   q_len (dev, nullable = 1 everywhere) [B]: the Lq_b of the storage rule that the page tables follow. It
+ *     need not be the number of tokens the call works on: tables laid out for a prefill of Lq queries at
+ *     length L stay valid, growing only at the end, while L and Lq are both counted up per decoded token;
+ *   cls (dev) [B*Hkv]: sink < 0 counts as 0, window < 1 as 1;
+ *   page_table (dev, int32) [page_table_len] (NULL only when that is 0), page_table_offs (dev, int32)
+ *     [B*Hkv+1], as everywhere.
+ *     A head whose table length disagrees with the storage rule sets SEGPAGED_STATUS_TABLE; a page id outside
+ *     [0, num_pages) sets SEGPAGED_STATUS_PAGE_ID. All accesses stay in bounds; what is computed for such a
+ *     head is undefined.
+ *
+ * 8-bit pools. k_pool and v_pool are [num_pages, P, D] bytes of codes, and kv_scale (16-byte aligned) is
+ * [num_pages, 2, P] exponent bytes, the K rows' before the V rows'. A row (the D values of one token and KV
+ * head) of codes c with exponent byte y stands for c * 2^(y-127). Writing rounds a bf16 row x with largest
+ * magnitude a: y - 127 is the smallest whole number >= -126 with a <= M * 2^(y-127), M = 448 (e4m3) or 127
+ * (int8), and c = x * 2^(127-y) rounded to nearest even (exact: the product with a power of two does not
+ * round). A row with an infinity or a NaN gets y = 255 and codes 0 and reads back as NaN. y = 0 reads as
+ * 2^-127.
+ * ------------------------------------------------------------------------------------------------ */
+
+/*
+ * segpaged_build into 8-bit pools (one kernel launch): arguments as there, plus the format and kv_scale.
+ * The rows stored are the quantised form of exactly the rows segpaged_build stores (RoPE re-alignment
+ * included, rounded to bf16 first); rows past L_b get codes 0 and y = 1. Pages not named by any table, and
+ * their exponent bytes, are not touched. Returns SEGPAGED_ERR_FORMAT for SEGPAGED_KV_BF16.
+ */
+int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format, const void* k_dense, const void* v_dense,
+                      const int32_t* cu_seqlens_k, const int32_t* q_len, const segpaged_head_class* cls,
+                      const int32_t* page_table, const int32_t* page_table_offs, const float* rope_cos_sin,
+                      void* k_pool, void* v_pool, uint8_t* kv_scale, int32_t* status, void* stream);
+
+/*
+ * Writes the new tokens' keys and values into their pages (one kernel launch), quantised for an 8-bit pool
+ * and copied for a bf16 one (kv_scale then ignored, may be NULL).
+ *   k_new, v_new (dev) [total_new, Hkv, D] bf16, 16-byte aligned, RoPE included.
+ *   cu_seqlens_new (dev) [B+1]: rows [cu[b], cu[b+1]) are the last tokens of sequence b, its positions
+ *     L_b - (cu[b+1] - cu[b]) .. L_b - 1. Rows of k_new outside [cu[0], cu[B]) are ignored. More rows than
+ *     L_b sets SEGPAGED_STATUS_TABLE and drops the rows before position 0.
+ * A row whose page a local head does not keep is dropped for that head. Nothing else in the pools changes.
+ */
+int segpaged_append(const segpaged_dims* dims, int32_t kv_format, const void* k_new, const void* v_new,
+                    int32_t total_new, const int32_t* cu_seqlens_new, const int32_t* ctx_len, const int32_t* q_len,
+                    const segpaged_head_class* cls, const int32_t* page_table, int64_t page_table_len,
+                    const int32_t* page_table_offs, void* k_pool, void* v_pool, uint8_t* kv_scale, int32_t* status,
+                    void* stream);
+
+/*
+ * Reads every stored page of 8-bit pools back into bf16 pools k_out, v_out (dev) [num_pages, P, D] at the same
+ * physical ids (one kernel launch), as the prefill-side calls take them: c * 2^(y-127) rounded to nearest even,
+ * which only rounds below the bf16 normal range. Rows past L_b are written as zero. Pages not named by any
+ * table are not touched. Returns SEGPAGED_ERR_FORMAT for SEGPAGED_KV_BF16. k_out and v_out must not overlap the
+ * 8-bit pools.
+ */
+int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_format, const int32_t* ctx_len, const int32_t* q_len,
+                           const segpaged_head_class* cls, const int32_t* page_table, int64_t page_table_len,
+                           const int32_t* page_table_offs, const void* k_pool, const void* v_pool,
+                           const uint8_t* kv_scale, void* k_out, void* v_out, int32_t* status, void* stream);
+
+/* Device scratch bytes segpaged_attn_decode needs. */
+size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims);
+
+/*
+ * Attention of each sequence's last token (position L_b - 1) over the keys its heads can see.
+ *   q (dev) [B, Hq, D] bf16; o (dev) [B, Hq, D] bf16; lse (dev) [Hq, B] float, natural log.
+ *   k_pool, v_pool, kv_scale (dev): pools of kv_format (kv_scale ignored for bf16, may be NULL). They hold the
+ *     token's own key and value already (segpaged_append, segpaged_build, segpaged_build_quant). Rows the token
+ *     cannot see (past L_b, outside sink and window) may hold anything, NaN included.
+ *   workspace (dev) >= segpaged_decode_workspace_bytes(dims), 16-byte aligned. A call owns it while it runs:
+ *     calls (or replayed graphs) that may overlap on the GPU need one each.
+ * A sequence with L_b = 0 (an unused batch slot) gets O = 0 and LSE = -infinity.
+ */
+int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format, const void* q, const void* k_pool,
+                         const void* v_pool, const uint8_t* kv_scale, const int32_t* page_table,
+                         int64_t page_table_len, const int32_t* page_table_offs, const int32_t* ctx_len,
+                         const int32_t* q_len, const segpaged_head_class* cls, float softmax_scale, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

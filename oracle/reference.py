@@ -300,6 +300,59 @@ def build_pool(k, v, cu_k, cu_q, is_global, sink, window, P, page_table, page_of
 
 
 # ----------------------------------------------------------------------------------------------
+# 8-bit rows (definition)
+# ----------------------------------------------------------------------------------------------
+
+CODE_MAX = {"e4m3": 448.0, "int8": 127.0}
+
+
+def e4m3_values() -> np.ndarray:
+    """fp64 value of each of the 256 e4m3 bytes: sign, 4 exponent bits (bias 7), 3 mantissa bits; exponent 0 is
+    subnormal, 0x7f and 0xff are NaN, there are no infinities."""
+    out = np.zeros(256)
+    for byte in range(256):
+        e, m = (byte >> 3) & 15, byte & 7
+        mag = (m / 8.0) * 2.0 ** -6 if e == 0 else (1 + m / 8.0) * 2.0 ** (e - 7)
+        out[byte] = (-mag if byte & 128 else mag) if (byte & 127) != 127 else np.nan
+    return out
+
+
+def _nearest_e4m3(y: np.ndarray) -> np.ndarray:
+    """Bytes of the e4m3 values nearest to y (|y| <= 448), ties to the even byte."""
+    mags = e4m3_values()[:127]
+    a = np.abs(y)
+    hi = np.clip(np.searchsorted(mags, a), 0, 126)
+    lo = np.maximum(hi - 1, 0)
+    d_hi, d_lo = mags[hi] - a, a - mags[lo]
+    pick = np.where((d_lo < d_hi) | ((d_lo == d_hi) & (lo % 2 == 0)), lo, hi)
+    pick = np.where(mags[hi] == a, hi, pick)
+    return (pick | np.where(np.signbit(y), 128, 0)).astype(np.uint8)
+
+
+def quantise_rows(x: np.ndarray, fmt: str):
+    """(codes uint8 bit patterns [..., D], exponent bytes uint8 [...]) of rows x [..., D], in fp64: the smallest whole
+    e >= -126 with max|x| <= M 2^e, then x 2^-e rounded to nearest, ties to even. A row that is not finite gets byte
+    255 and zero codes."""
+    x = np.asarray(x, np.float64)
+    bad = ~np.isfinite(x).all(-1)
+    x = np.where(bad[..., None], 0.0, x)
+    top = np.abs(x).max(-1)
+    e = np.full(top.shape, -126, np.int64)
+    for k in range(-126, 128):
+        e = np.where(top > CODE_MAX[fmt] * 2.0 ** k, k + 1, e)
+    y = x * 2.0 ** (-e[..., None].astype(np.float64))
+    codes = _nearest_e4m3(y) if fmt == "e4m3" else np.rint(y).astype(np.int8).view(np.uint8)
+    return codes, np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def dequantise_rows(codes: np.ndarray, y: np.ndarray, fmt: str) -> np.ndarray:
+    """fp64 values of rows of 8-bit codes [..., D] with exponent bytes [...] (255: NaN)."""
+    v = e4m3_values()[codes] if fmt == "e4m3" else codes.view(np.int8).astype(np.float64)
+    s = np.where(y == 255, np.nan, 2.0 ** (y.astype(np.float64) - 127.0))
+    return v * s[..., None]
+
+
+# ----------------------------------------------------------------------------------------------
 # C oracle (brute-force visible set, OpenMP over rows)
 # ----------------------------------------------------------------------------------------------
 
