@@ -1,18 +1,51 @@
 // decode_sm100.cuh -- attention of one new token per sequence over its own stored pages.
+//
+// For sequence b, KV head k and the G query heads h of its group, at position i = L - 1:
+//   s_j = scale q_h . k_j over the visible keys j,  O_h = sum_j softmax(s)_j v_j,  LSE_h = ln sum_j exp(s_j).
+// Every visible key and value is read once and used by G heads only, so the call is bound by HBM (for G = 8, 16
+// flops per bf16 byte; the tensor cores pass 60 flops per byte here even through mma.sync). What matters is that
+// all SMs load all the time. So:
+//   - The work is the list of 128-token tiles of all (sequence, KV head) pairs, cut into one equal run of tiles per
+//     CTA (one persistent CTA per SM): a pair's tiles may end in one CTA and go on in the next. Each CTA finds its run
+//     by itself from ctx_len and the classes in device memory (a prefix sum over the pairs, 1-2 us), so a captured
+//     call follows the lengths and there is no host plan. Runs that end inside a pair leave a partial result
+//     (O / l and its log2-sum) in the workspace, which decode_combine_kernel joins in tile order: no atomics, and the
+//     result depends on the lengths and the grid only.
+//   - A producer warp streams the tiles through a ring of shared-memory stages with TMA (page id = coordinate), up to
+//     three (bf16) or six (8-bit) 128-token tiles ahead, across pair boundaries, with the page ids of the next tile
+//     fetched while it waits for a free stage.
+//   - Eight consumer warps take 16 tokens of each tile, and keep their own running maximum, sum and O in registers;
+//     they meet only where a pair ends. S^T = K Q^T puts the tokens on the 16 rows of mma.m16n8k16 and the heads on
+//     its 8 columns, so up to 8 heads cost the same and nothing is padded from 8 to 16; O^T = V^T P^T likewise.
+//   - tcgen05 would need the tile's rows as its 128-row M and TMEM round trips for an S of 128 x 8; the work is a
+//     sixth of what mma.sync can do in the time the bytes take, so the legacy path is the shorter one here.
+// 8-bit pools: codes become fp16 in registers (exact). Query rows are brought to a largest magnitude of 2^15 by a power
+// of two first, so that bf16 queries of any size are exact in fp16 to 2^-29 of the row's largest. The K row's exponent
+// scales the logit; the V row's exponent 2^(y - r), r the largest one so far in this warp, multiplies the
+// probability, and O is kept in units of 2^(r - 14): the product, at most 2^14, is rounded to fp16 (2^-11 relative
+// down to 2^-28 of the largest). bf16 pools: a probability is split into a sum of two bf16 (2^-16 relative), which
+// costs a second V product where the tensor pipe idles.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "plan.h"
 #include "quant_pages.cuh"
+#include "quant_rows.cuh"
 #include "sm100_ptx.cuh"
 
 namespace segpaged {
 
+constexpr int kDecodeTile = 128;         // tokens of a tile
+constexpr int kDecodeWarps = 8;          // consumer warps, 16 tokens of a tile each
+constexpr int kDecodeThreads = 32 * (kDecodeWarps + 1);
+constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
+constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
+constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
+
 struct DecodeParams {
   const __nv_bfloat16* q;      // [B][Hq][D]
-  const uint8_t* k_pool;       // [num_pages][P][D], bf16 or codes
-  const uint8_t* v_pool;
   const uint8_t* kv_scale;     // [num_pages][2][P], null for bf16
   const int32_t* table;
   const int32_t* offs;         // [B*Hkv+1]
@@ -21,70 +54,687 @@ struct DecodeParams {
   const int32_t* cls;          // [B*Hkv][3]
   __nv_bfloat16* o;            // [B][Hq][D]
   float* lse;                  // [Hq][B]
+  float* part_o;               // [2 x CTAs][16][D]: O / l of a chunk
+  float* part_lse;             // [2 x CTAs][16]: its log2 sum
+  int32_t* part_meta;          // [CTAs][2]: pair and chunk count of the pair whose first chunk is this CTA's last
   int32_t* status;             // nullable
   int64_t table_len;
-  int32_t B, Hkv, G, P, num_pages;
+  int32_t B, Hkv, G, log2_page, num_pages;
+  int32_t hg;                  // passes of a group: max(1, G / 16)
   float scale_log2;
 };
 
-// One warp per (sequence, query head): lanes split the row, tokens one after the other.
-template <int D, int FMT>
-__global__ void __launch_bounds__(128) decode_kernel(DecodeParams p) {
-  constexpr int E = D / 32;  // elements of a lane
-  const int lane = threadIdx.x & 31;
-  const int Hq = p.Hkv * p.G;
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (w >= (int64_t)p.B * Hq) return;
-  const int b = (int)(w / Hq), h = (int)(w % Hq), bk = b * p.Hkv + h / p.G;
-  int32_t L;
-  const Split sp = device_split(p.ctx_len, p.q_len, p.cls, b, bk, p.P, 1, &L);
-  const int32_t sink = p.cls[3 * bk] ? L : max(p.cls[3 * bk + 1], 0), lo = L - max(p.cls[3 * bk + 2], 1);
-  const int64_t off = p.offs[bk], n = (int64_t)p.offs[bk + 1] - off;
-  if (n != sp.total && lane == 0) report(p.status, 2);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < E; ++i) {
-    q[i] = __bfloat162float(p.q[w * D + lane * E + i]) * p.scale_log2;
-    o[i] = 0.f;
-  }
-  for (int32_t t = 0; t < sp.total; ++t) {
-    const int32_t lp = t < sp.n_sink ? t : sp.w0 + (t - sp.n_sink);
-    int32_t pid = 0;
-    if (t < n && off >= 0 && off + t < p.table_len) pid = p.table[off + t];
-    else if (lane == 0) report(p.status, 2);
-    if (pid < 0 || pid >= p.num_pages) {
-      if (lane == 0) report(p.status, 1);
-      pid = 0;
+template <int D, int FMT, int NB>
+struct DecodeCfg {
+  static constexpr int EB = FMT == kFmtBf16 ? 2 : 1;             // bytes of an element
+  static constexpr int ROWB = D * EB < 128 ? D * EB : 128;       // bytes of a row in one column block
+  static constexpr int CB = D * EB / ROWB;                       // column blocks
+  static constexpr int BLOCK_BYTES = kDecodeTile * ROWB;
+  static constexpr int TILE_BYTES = CB * BLOCK_BYTES;            // K or V
+  static constexpr int SCALE_BYTES = FMT == kFmtBf16 ? 0 : 2 * kDecodeTile;
+  static constexpr int Q_BYTES = NB * 8 * D * 2;
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int EXTRA_BYTES = SCALE_BYTES + Q_BYTES;      // beside a stage: exponent bytes, query rows
+  static constexpr int MERGE_BYTES = kDecodeWarps / 2 * 8 * D * 4;
+  static constexpr int FIXED_BYTES = MERGE_BYTES + 2048 + 1024;  // + barriers and small arrays + alignment slack
+  static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
+  static_assert(STAGES >= 2, "ring");
+};
+
+// What a consumer needs to know of a tile.
+struct DecodeTileHeader {
+  int32_t v0, v1;   // visible rows [v0, v1) of the tile
+  int32_t pair;     // pair index (sequence, KV head, pass)
+  int32_t flags;    // bit 0: first tile of a chunk, bit 1: last; bits 2..: 1 + partial slot, 0: the whole pair
+};
+
+// Tiles of one (sequence, KV head): [0, n_a) cover tokens [0, a1), the others [b0, L) of which [lo, L) are visible.
+struct DecodeGeom {
+  int32_t L, a1, b0, lo, n_a, n;
+};
+
+__device__ __forceinline__ DecodeGeom decode_geom(const DecodeParams& p, int32_t bk) {
+  DecodeGeom g;
+  const int b = bk / p.Hkv;
+  g.L = max(p.ctx_len[b], 0);
+  const bool global = p.cls[3 * bk] != 0;
+  const int32_t sink = min(max(p.cls[3 * bk + 1], 0), g.L), win = max(p.cls[3 * bk + 2], 1);
+  g.lo = max(g.L - win, 0);
+  g.a1 = sink;
+  if (global || sink >= g.lo) g.a1 = g.lo = 0;  // one run of visible tokens
+  g.b0 = (g.lo >> p.log2_page) << p.log2_page;
+  g.n_a = (g.a1 + kDecodeTile - 1) / kDecodeTile;
+  g.n = g.n_a + (int32_t)(((int64_t)g.L - g.b0 + kDecodeTile - 1) / kDecodeTile);
+  return g;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  const __half2 h = codes_to_half2<FMT>(w);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 2^e for e <= 127; 0 below the normal range.
+__device__ __forceinline__ float exp2_int(int32_t e) { return __uint_as_float((uint32_t)max(e + 127, 0) << 23); }
+
+// Bulk copy of `bytes` (a multiple of 16) contiguous bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   ptx::smem_addr(dst)),
+               "l"((uint64_t)__cvta_generic_to_global(src)), "r"(bytes), "r"(ptx::smem_addr(bar))
+               : "memory");
+}
+
+// A bounded wait of a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, status, kDecodeStatusTimeout));
+}
+
+// Shared memory beside the ring (2048 bytes).
+struct DecodeSmall {
+  uint64_t full[8], empty[8];
+  uint64_t sync;                                // consumers' meeting point
+  DecodeTileHeader hdr[8];
+  float m[kDecodeWarps][16], l[kDecodeWarps][16];
+  long long warp_sum[kDecodeWarps + 1];
+  long long start, total;                       // this CTA's first tile, tiles in all
+  int32_t pair0, tile0;                         // where its first tile lies
+  int32_t abort;
+};
+static_assert(sizeof(DecodeSmall) <= 2048, "small shared arrays");
+
+// Producer's place in the list of tiles.
+struct DecodeCursor {
+  int32_t pair, tile, bk;
+  DecodeGeom g;
+  int64_t off, len;  // the head's page table: first entry, entries
+  int32_t n_sink, w0;
+};
+
+template <int D, int FMT, int NB>
+__global__ void __launch_bounds__(kDecodeThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const DecodeParams p) {
+  using C = DecodeCfg<D, FMT, NB>;
+  constexpr bool BF = FMT == kFmtBf16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* extras = ring + C::STAGES * C::STAGE_BYTES;
+  float* merge = reinterpret_cast<float*>(extras + C::STAGES * C::EXTRA_BYTES);
+  DecodeSmall& sm = *reinterpret_cast<DecodeSmall*>(extras + C::STAGES * C::EXTRA_BYTES + C::MERGE_BYTES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t cta = blockIdx.x;
+  const int32_t pairs = p.B * p.Hkv * p.hg;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      ptx::mbar_init(&sm.full[s], 1);
+      ptx::mbar_init(&sm.empty[s], kDecodeWarps);
     }
-    for (int32_t r = 0; r < p.P; ++r) {
-      const int32_t tok = lp * p.P + r;
-      if (tok >= L || (tok >= sink && tok < lo)) continue;
-      const int64_t at = ((int64_t)pid * p.P + r) * D + lane * E;
-      float s = 0.f, v[E], ks = 1.f, vs = 1.f;
-      if (FMT != kFmtBf16) {
-        ks = row_scale(p.kv_scale[(int64_t)pid * 2 * p.P + r]);
-        vs = row_scale(p.kv_scale[(int64_t)pid * 2 * p.P + p.P + r]);
+    ptx::mbar_init(&sm.sync, kDecodeWarps);
+    ptx::mbar_fence_init();
+    sm.abort = 0;
+    ptx::tma_prefetch_desc(&tk);
+    ptx::tma_prefetch_desc(&tv);
+  }
+
+  // ---- this CTA's run of tiles: prefix sum over the pairs
+  const int32_t per = (pairs + kDecodeThreads - 1) / kDecodeThreads;
+  const int32_t u_lo = min((int32_t)threadIdx.x * per, pairs), u_hi = min(u_lo + per, pairs);
+  long long mine = 0;
+  for (int32_t u = u_lo; u < u_hi; ++u) mine += decode_geom(p, u / p.hg).n;
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += x;
+  }
+  if (lane == 31) sm.warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w <= kDecodeWarps; ++w) {
+    if (w < warp) before += sm.warp_sum[w];
+    total += sm.warp_sum[w];
+  }
+  const int32_t ctas = (int32_t)min((long long)gridDim.x, max(total, 1ll));  // each of these has a tile
+  const long long start = cta < ctas ? total * cta / ctas : total, end = cta < ctas ? total * (cta + 1) / ctas : total;
+  if (start < end && start >= before && start < before + mine) {
+    long long at = before;
+    for (int32_t u = u_lo; u < u_hi; ++u) {
+      const int32_t n = decode_geom(p, u / p.hg).n;
+      if (start < at + n) {
+        sm.pair0 = u;
+        sm.tile0 = (int32_t)(start - at);
+        break;
       }
-      for (int i = 0; i < E; ++i) {
-        float k;
-        if (FMT == kFmtBf16) {
-          k = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.k_pool)[at + i]);
-          v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v_pool)[at + i]);
-        } else {
-          k = __low2float(codes_to_half2<FMT>(p.k_pool[at + i]));
-          v[i] = __low2float(codes_to_half2<FMT>(p.v_pool[at + i])) * vs;
+      at += n;
+    }
+  }
+  // pairs without a visible key (an empty sequence): O = 0, LSE = -inf, written by one CTA each
+  const int32_t heads = min(p.G, kDecodeGroup), Hq = p.Hkv * p.G;
+  for (int32_t u = u_lo; u < u_hi; ++u) {
+    const int32_t bk = u / p.hg, b = bk / p.Hkv;
+    if (u % (int32_t)gridDim.x != cta || p.ctx_len[b] > 0) continue;
+    const int32_t h0 = (bk % p.Hkv) * p.G + (u % p.hg) * kDecodeGroup;
+    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)b * Hq + h0) * D);
+    for (int i = 0; i < heads * D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+    for (int h = 0; h < heads; ++h) p.lse[(int64_t)(h0 + h) * p.B + b] = -INFINITY;
+  }
+  if (threadIdx.x == 0) {
+    p.part_meta[2 * cta] = 0;
+    p.part_meta[2 * cta + 1] = 0;
+  }
+  __syncthreads();
+  const int32_t tiles = (int32_t)(end - start);
+
+  if (warp == kDecodeWarps) {
+    // ------------------------------------------------------------------------------------ producer
+    const int32_t page = 1 << p.log2_page;
+    const int32_t log2_box = min(p.log2_page, 6), box = 1 << log2_box;  // rows of one TMA box
+    const uint32_t boxes = kDecodeTile >> log2_box;
+    DecodeCursor c = {};
+    auto open_pair = [&](int32_t u) {
+      c.pair = u;
+      c.bk = u / p.hg;
+      c.g = decode_geom(p, c.bk);
+      const Split s = device_split(p.ctx_len, p.q_len, p.cls, c.bk / p.Hkv, c.bk, page, 1, &c.g.L);
+      c.off = p.offs[c.bk];
+      c.len = (int64_t)p.offs[c.bk + 1] - c.off;
+      c.n_sink = s.n_sink;
+      c.w0 = s.w0;
+      if (c.len != s.total && lane == 0) report(p.status, 2);
+    };
+    // First token of the cursor's tile and its visible tokens.
+    auto span = [&](int32_t& t0, int32_t& lo, int32_t& hi) {
+      const bool sink = c.tile < c.g.n_a;
+      t0 = sink ? c.tile * kDecodeTile : c.g.b0 + (c.tile - c.g.n_a) * kDecodeTile;
+      lo = max(t0, sink ? 0 : c.g.lo);
+      hi = (int32_t)min((int64_t)t0 + kDecodeTile, (int64_t)(sink ? c.g.a1 : c.g.L));
+    };
+    // Whether a visible token lies in this lane's box of the tile, and the page it is on (a load that nothing waits
+    // for before the page is used).
+    auto fetch = [&](bool& need) -> int32_t {
+      int32_t t0, lo, hi;
+      span(t0, lo, hi);
+      const int64_t tok = (int64_t)t0 + lane * box;
+      need = (uint32_t)lane < boxes && tok + box > lo && tok < hi;
+      if (!need) return 0;
+      const int32_t lp = (int32_t)(tok >> p.log2_page), t = lp < c.n_sink ? lp : lp - c.w0 + c.n_sink;
+      if (t >= c.len || c.off < 0 || c.off + t >= p.table_len) {
+        report(p.status, 2);
+        return 0;
+      }
+      return __ldg(p.table + c.off + t);
+    };
+    if (tiles > 0) {
+      open_pair(sm.pair0);
+      c.tile = sm.tile0;
+      bool need, first = true;
+      int32_t id = fetch(need);
+      uint32_t issued = 0;
+      for (int32_t i = 0; i < tiles; ++i) {
+        const int s = i % C::STAGES;
+        uint8_t* stage = ring + s * C::STAGE_BYTES;
+        uint8_t* extra = extras + s * C::EXTRA_BYTES;
+        int32_t t0, lo, hi;
+        span(t0, lo, hi);
+        const bool last = i + 1 == tiles || c.tile + 1 == c.g.n;
+        DecodeTileHeader h;
+        h.v0 = lo - t0;
+        h.v1 = hi - t0;
+        h.pair = c.pair;
+        h.flags = (first ? 1 : 0) | (last ? 2 : 0);
+        if (last) {
+          const bool from_start = c.tile <= i;  // the chunk holds the pair's tile 0
+          const bool to_end = c.tile + 1 == c.g.n;
+          if (!(from_start && to_end)) h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
+          if (from_start && !to_end && lane == 0) {
+            // the pair goes on in the CTAs after this one, to the CTA that holds its last tile
+            const long long end_tile = start + i - c.tile + c.g.n;  // one past it, in the list of all tiles
+            p.part_meta[2 * cta] = c.pair;
+            p.part_meta[2 * cta + 1] = (int32_t)((end_tile * ctas - 1) / total) - cta + 1;
+          }
         }
-        s += q[i] * k;
+        int32_t pid = id;
+        const bool load = need;
+        // the next tile's page ids are on their way while this one waits for its stage
+        const int32_t this_bk = c.bk, this_pair = c.pair;
+        const bool this_first = first;
+        first = last;
+        if (i + 1 < tiles) {
+          if (++c.tile == c.g.n) {
+            int32_t u = c.pair + 1;
+            while (u < pairs && decode_geom(p, u / p.hg).n == 0) ++u;
+            if (u >= pairs) {  // only if the lengths changed while this call runs
+              sm.abort = 1;
+              break;
+            }
+            open_pair(u);
+            c.tile = 0;
+          }
+          id = fetch(need);
+        }
+        if (i >= C::STAGES && !warp_wait(&sm.empty[s], ((i / C::STAGES) - 1) & 1, &sm.abort, p.status))
+          break;
+        if (load && (uint32_t)pid >= (uint32_t)p.num_pages) {
+          report(p.status, 1);
+          pid = 0;
+        }
+        const uint32_t have = __ballot_sync(0xffffffffu, load);
+        const uint32_t boxes_in_page = 1u << (p.log2_page - log2_box);
+        // one exponent copy per page: by the page's first box that is loaded
+        const uint32_t before_it = boxes_in_page == 1 ? 0u : ((1u << (lane & 1)) - 1u) << (lane & 30);
+        const bool scales = !BF && load && (have & before_it) == 0;
+        const uint32_t n_scales = BF ? 0 : __popc(__ballot_sync(0xffffffffu, scales));
+        if (lane == 0) {
+          sm.hdr[s] = h;
+          const uint32_t bytes = __popc(have) * 2 * box * D * C::EB + n_scales * 2 * page + (this_first ? heads * D * 2 : 0);
+          ptx::mbar_arrive_expect_tx(&sm.full[s], bytes);
+          if (this_first) {
+            const int32_t b = this_bk / p.Hkv, h0 = (this_bk % p.Hkv) * p.G + (this_pair % p.hg) * kDecodeGroup;
+            bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)b * Hq + h0) * D, heads * D * 2, &sm.full[s]);
+          }
+        }
+        issued = i + 1;
+        __syncwarp();
+        if (load) {
+          const int32_t row = (int32_t)((t0 + lane * box) & (page - 1));
+#pragma unroll
+          for (int cb = 0; cb < C::CB; ++cb) {
+            const int at = cb * C::BLOCK_BYTES + lane * box * C::ROWB;
+            ptx::tma_load_3d(stage + at, &tk, cb * (C::ROWB / C::EB), row, pid, &sm.full[s]);
+            ptx::tma_load_3d(stage + C::TILE_BYTES + at, &tv, cb * (C::ROWB / C::EB), row, pid, &sm.full[s]);
+          }
+          if (scales)
+            bulk_load(extra + (lane * box / page) * 2 * page, p.kv_scale + (int64_t)pid * 2 * page, 2 * page, &sm.full[s]);
+        }
+        __syncwarp();
       }
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= ks;
-      const float mn = fmaxf(m, s), a = m == -INFINITY ? 0.f : exp2f(m - mn), pr = exp2f(s - mn);
-      l = l * a + pr;
-      for (int i = 0; i < E; ++i) o[i] = o[i] * a + pr * v[i];
-      m = mn;
+      // after a timeout: the copies in flight land before the block's memory is given up
+      if (sm.abort)
+        for (uint32_t i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
+          ptx::mbar_wait(&sm.full[i % C::STAGES], (i / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
+    }
+  } else {
+    // ----------------------------------------------------------------------------------- consumers
+    constexpr int KS = D / 16;  // k16 steps of a logit, and m16 tiles of O^T
+    const int g = lane >> 2, t = lane & 3;
+    const int row0 = warp * 16;
+    // ldmatrix row of this lane: rows 0-7 / 8-15 of the warp's tokens, chunk parity, for K (and bf16 / 8-bit V)
+    const int lrow = row0 + (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
+    const int trow = row0 + (lane & 7) + (lane >> 4) * 8, tchunk = (lane >> 3) & 1;  // bf16 V, transposed
+    auto chunk_addr = [](uint32_t base, int row, int chunk) {  // 16-byte chunk of a row in the swizzled tile
+      if (C::ROWB == 128)
+        return base + (chunk >> 3) * C::BLOCK_BYTES + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+      return base + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+    };
+    uint32_t qf[NB][KS][2];
+    float head_scale[NB][2];                     // multiplies the logits of heads 2t, 2t + 1
+    float m[NB][2], l[NB][2], o[NB][KS][4];
+    int32_t vref = 0;                            // r + 127
+    uint32_t meets = 0;
+    bool ok = true;
+    auto meet = [&]() {                          // all consumer warps (bounded, unlike a block barrier)
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.sync);
+      ok = warp_wait(&sm.sync, meets++ & 1, &sm.abort, p.status);
+      return ok;
+    };
+    for (int32_t i = 0; i < tiles && ok; ++i) {
+      const int s = i % C::STAGES;
+      if (!warp_wait(&sm.full[s], (i / C::STAGES) & 1, &sm.abort, p.status)) break;
+      const DecodeTileHeader h = sm.hdr[s];
+      const uint32_t kbase = ptx::smem_addr(ring + s * C::STAGE_BYTES), vbase = kbase + C::TILE_BYTES;
+      const uint8_t* extra = extras + s * C::EXTRA_BYTES;
+      if (h.flags & 1) {
+        // ---- a chunk begins: query fragments, running values
+        const __nv_bfloat16* qs = reinterpret_cast<const __nv_bfloat16*>(extra + C::SCALE_BYTES);
+        vref = 0;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int head = nb * 8 + g;
+          uint32_t top = 0;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // fp16: the contraction runs in the order the code bytes lie in, 4t .. 4t+3 of each 16
+              const int d = 16 * ks + (BF ? 2 * t + 8 * j : 4 * t + 2 * j);
+              qf[nb][ks][j] = head < heads ? *reinterpret_cast<const uint32_t*>(qs + head * D + d) : 0u;
+              top = absmax2(top, qf[nb][ks][j]);
+            }
+          }
+          if (BF) {
+            head_scale[nb][0] = head_scale[nb][1] = p.scale_log2;
+          } else {
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int32_t biased = (int32_t)(max(top & 0xffffu, top >> 16) >> 7);
+            const int32_t e = biased == 255 ? 0 : 15 - max(biased - 127, -100);  // not finite: as it is
+            const float up = exp2_int(e);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                qf[nb][ks][j] = pack_f16x2(bf16_lo(qf[nb][ks][j]) * up, bf16_hi(qf[nb][ks][j]) * up);
+            const float back = p.scale_log2 * exp2_int(-e);
+            head_scale[nb][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+            head_scale[nb][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            m[nb][j] = -INFINITY;
+            l[nb][j] = 0.f;
+          }
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) o[nb][mt][0] = o[nb][mt][1] = o[nb][mt][2] = o[nb][mt][3] = 0.f;
+        }
+      }
+      if (row0 + 16 > h.v0 && row0 < h.v1) {
+        const bool edge = row0 < h.v0 || row0 + 16 > h.v1;
+        // ---- logits: rows = tokens g, g + 8; columns = heads 2t, 2t + 1
+        float sc[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+        if (BF) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a[4];
+            ldsm4(chunk_addr(kbase, lrow, 2 * ks + lchunk), a);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<true>(sc[nb], a[0], a[1], a[2], a[3], qf[nb][ks][0], qf[nb][ks][1]);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ks += 2) {
+            uint32_t a[4];
+            ldsm4(chunk_addr(kbase, lrow, ks + lchunk), a);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a0 = codes2<FMT>(a[2 * j]), a2 = codes2<FMT>(a[2 * j] >> 16);
+              const uint32_t a1 = codes2<FMT>(a[2 * j + 1]), a3 = codes2<FMT>(a[2 * j + 1] >> 16);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<false>(sc[nb], a0, a1, a2, a3, qf[nb][ks + j][0], qf[nb][ks + j][1]);
+            }
+          }
+        }
+        const int r0 = row0 + g, r1 = r0 + 8;
+        const bool in0 = r0 >= h.v0 && r0 < h.v1, in1 = r1 >= h.v0 && r1 < h.v1;
+        float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f, vshift = 1.f;
+        if (!BF) {
+          const int page = 1 << p.log2_page;  // exponent bytes: [page of the tile][K, V][row]
+          const int at = (row0 >> p.log2_page) * page * 2 + (row0 & (page - 1)) + g;
+          ks0 = row_scale(extra[at]);
+          ks1 = row_scale(extra[at + 8]);
+          const int32_t y0 = extra[at + page], y1 = extra[at + 8 + page];
+          int32_t top = max(in0 && y0 != kRowNaN ? y0 : 0, in1 && y1 != kRowNaN ? y1 : 0);
+          top = max(vref, __reduce_max_sync(0xffffffffu, top));
+          vshift = exp2_int(vref - top);
+          vref = top;
+          vs0 = y0 == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(y0 - top + 14);
+          vs1 = y1 == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(y1 - top + 14);
+        }
+        uint32_t pf[NB][2], pl[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float f0 = head_scale[nb][0], f1 = head_scale[nb][1];
+          float x0 = sc[nb][0] * (ks0 * f0), x1 = sc[nb][1] * (ks0 * f1);
+          float x2 = sc[nb][2] * (ks1 * f0), x3 = sc[nb][3] * (ks1 * f1);
+          if (edge) {
+            x0 = in0 ? x0 : -INFINITY;
+            x1 = in0 ? x1 : -INFINITY;
+            x2 = in1 ? x2 : -INFINITY;
+            x3 = in1 ? x3 : -INFINITY;
+          }
+          float n0 = fmaxf(x0, x2), n1 = fmaxf(x1, x3);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, d));
+          }
+          n0 = fmaxf(n0, m[nb][0]);
+          n1 = fmaxf(n1, m[nb][1]);
+          // a larger maximum (or V exponent) rescales what was summed so far
+          if (__any_sync(0xffffffffu, n0 != m[nb][0] || n1 != m[nb][1] || vshift != 1.f)) {
+            const float c0 = m[nb][0] == -INFINITY ? 0.f : ptx::ex2(m[nb][0] - n0);
+            const float c1 = m[nb][1] == -INFINITY ? 0.f : ptx::ex2(m[nb][1] - n1);
+            // NaN sums stay NaN: 0 * NaN
+            l[nb][0] *= c0;
+            l[nb][1] *= c1;
+            const float w0 = c0 * vshift, w1 = c1 * vshift;
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+              o[nb][mt][0] *= w0;
+              o[nb][mt][1] *= w1;
+              o[nb][mt][2] *= w0;
+              o[nb][mt][3] *= w1;
+            }
+            m[nb][0] = n0;
+            m[nb][1] = n1;
+          }
+          const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
+          float p0 = ptx::ex2(x0 - b0), p1 = ptx::ex2(x1 - b1), p2 = ptx::ex2(x2 - b0), p3 = ptx::ex2(x3 - b1);
+          l[nb][0] += p0 + p2;
+          l[nb][1] += p1 + p3;
+          if (BF) {
+            const uint32_t h0 = ptx::pack_bf16x2(p0, p1), h1 = ptx::pack_bf16x2(p2, p3);
+            pf[nb][0] = transpose8x8(h0);
+            pf[nb][1] = transpose8x8(h1);
+            pl[nb][0] = transpose8x8(ptx::pack_bf16x2(p0 - bf16_lo(h0), p1 - bf16_hi(h0)));
+            pl[nb][1] = transpose8x8(ptx::pack_bf16x2(p2 - bf16_lo(h1), p3 - bf16_hi(h1)));
+          } else {
+            // a masked token's exponent byte may be anything: its weight is zero whatever that says
+            const float w0 = edge && !in0 ? 0.f : vs0, w1 = edge && !in1 ? 0.f : vs1;
+            pf[nb][0] = transpose8x8(pack_f16x2(p0 * w0, p1 * w0));
+            pf[nb][1] = transpose8x8(pack_f16x2(p2 * w1, p3 * w1));
+          }
+        }
+        // ---- O^T += V^T P^T. Rows outside [v0, v1) may hold NaN: their bits are cleared (tokens 2t, 2t+1 | +8)
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (edge) {
+          auto halves = [&](int r) {
+            return (r >= h.v0 && r < h.v1 ? 0xffffu : 0u) | (r + 1 >= h.v0 && r + 1 < h.v1 ? 0xffff0000u : 0u);
+          };
+          keep0 = halves(row0 + 2 * t);
+          keep1 = halves(row0 + 2 * t + 8);
+        }
+        if (BF) {
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            uint32_t a[4];
+            ldsm4_t(chunk_addr(vbase, trow, 2 * mt + tchunk), a);
+            if (edge) {
+              a[0] &= keep0;
+              a[1] &= keep0;
+              a[2] &= keep1;
+              a[3] &= keep1;
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816<true>(o[nb][mt], a[0], a[1], a[2], a[3], pf[nb][0], pf[nb][1]);
+              mma16816<true>(o[nb][mt], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < KS; mt += 2) {
+            uint32_t a[4];
+            ldsm4_t(chunk_addr(vbase, lrow, mt + lchunk), a);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // bytes of a register: token 2t's codes of dims 2g, 2g+1, then token 2t+1's
+              const uint32_t x = __byte_perm(a[2 * j], 0, 0x3120), y = __byte_perm(a[2 * j + 1], 0, 0x3120);
+              uint32_t a0 = codes2<FMT>(x), a1 = codes2<FMT>(x >> 16), a2 = codes2<FMT>(y), a3 = codes2<FMT>(y >> 16);
+              if (edge) {
+                a0 &= keep0;
+                a1 &= keep0;
+                a2 &= keep1;
+                a3 &= keep1;
+              }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16816<false>(o[nb][mt + j], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);  // this warp has read its rows
+      if (!(h.flags & 2)) continue;
+
+      // ---- a chunk ends: the eight warps' results become one
+      const int32_t bk = h.pair / p.hg, b = bk / p.Hkv;
+      const int32_t h0 = (bk % p.Hkv) * p.G + (h.pair % p.hg) * kDecodeGroup;
+      const int32_t slot = (h.flags >> 2) - 1;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
+          if (g == 0) {
+            sm.m[warp][nb * 8 + 2 * t + j] = m[nb][j];
+            sm.l[warp][nb * 8 + 2 * t + j] = l[nb][j];
+          }
+        }
+      if (!meet()) break;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float top[2], sum[2], w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int head = nb * 8 + 2 * t + j;
+          top[j] = -INFINITY;
+          for (int x = 0; x < kDecodeWarps; ++x) top[j] = fmaxf(top[j], sm.m[x][head]);
+          sum[j] = 0.f;
+          for (int x = 0; x < kDecodeWarps; ++x) {
+            const float mx = sm.m[x][head];
+            sum[j] += (mx == -INFINITY ? 0.f : ptx::ex2(mx - top[j])) * sm.l[x][head];
+          }
+          w[j] = m[nb][j] == -INFINITY ? 0.f : ptx::ex2(m[nb][j] - top[j]);
+          if (!BF) w[j] *= exp2_int(vref - 127 - 14);
+        }
+        float* mine_m = merge + (warp & 3) * (KS * 128) + lane;
+        if (warp >= 4)
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mine_m[(mt * 4 + c) * 32] = o[nb][mt][c] * w[c & 1];
+        if (!meet()) break;
+        if (warp < 4)
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mine_m[(mt * 4 + c) * 32] += o[nb][mt][c] * w[c & 1];
+        if (!meet()) break;
+        // warp x finishes the 16 dims of m-tile x; this lane's heads are again 2t, 2t + 1
+        if (warp < KS) {
+          float v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float* from = merge + (warp * 4 + c) * 32 + lane;
+            v[c] = (from[0] + from[KS * 128]) + (from[2 * KS * 128] + from[3 * KS * 128]);
+          }
+          const int d0 = 16 * warp + (BF ? g : 2 * g), d1 = d0 + (BF ? 8 : 1);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int head = nb * 8 + 2 * t + j;
+            if (head >= heads) continue;
+            const float inv = 1.f / sum[j];
+            if (slot < 0) {
+              __nv_bfloat16* out = p.o + ((int64_t)b * Hq + h0 + head) * D;
+              out[d0] = __float2bfloat16_rn(v[j] * inv);
+              out[d1] = __float2bfloat16_rn(v[2 + j] * inv);
+            } else {
+              float* out = p.part_o + ((int64_t)slot * kDecodeGroup + head) * D;
+              out[d0] = v[j] * inv;
+              out[d1] = v[2 + j] * inv;
+            }
+            if (warp == 0 && g == 0) {
+              const float lse2 = top[j] + log2f(sum[j]);
+              if (slot < 0) p.lse[(int64_t)(h0 + head) * p.B + b] = 0.6931471805599453f * lse2;
+              else p.part_lse[(int64_t)slot * kDecodeGroup + head] = lse2;
+            }
+          }
+        }
+        if (nb + 1 < NB && !meet()) break;  // the buffer is free again
+      }
+      if (ok) meet();  // as are the buffer and sm.m, sm.l for the next chunk
     }
   }
-  for (int i = 0; i < E; ++i) p.o[w * D + lane * E + i] = __float2bfloat16_rn(L > 0 ? o[i] / l : 0.f);
-  if (lane == 0) p.lse[(int64_t)h * p.B + b] = L > 0 ? 0.6931471805599453f * (m + log2f(l)) : -INFINITY;
+  __syncthreads();
+}
+
+// Joins the chunks of the pairs that several CTAs shared: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
+// Block (c, head) does the pair whose first chunk CTA c left; its other chunks lie in the first slots of the CTAs
+// after it. Eight groups of D threads take every eighth chunk each and are merged in order.
+template <int D>
+__global__ void __launch_bounds__(8 * D) decode_combine_kernel(const DecodeParams p) {
+  __shared__ float s_m[8], s_l[8], s_o[8][D];
+  const int32_t cta = blockIdx.x, head = blockIdx.y;
+  const int32_t pair = p.part_meta[2 * cta], n = p.part_meta[2 * cta + 1];
+  if (n <= 1) return;
+  const int d = threadIdx.x % D, grp = threadIdx.x / D;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int32_t c = grp; c < n; c += 8) {
+    const int64_t at = (int64_t)(c == 0 ? 2 * cta + 1 : 2 * (cta + c)) * kDecodeGroup + head;
+    const float lc = p.part_lse[at], oc = p.part_o[at * D + d];
+    if (lc == -INFINITY) continue;
+    const float mn = fmaxf(m, lc), a = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(lc - mn);
+    l = l * a + w;
+    o = o * a + w * oc;
+    m = mn;
+  }
+  s_o[grp][d] = o;
+  if (d == 0) {
+    s_m[grp] = m;
+    s_l[grp] = l;
+  }
+  __syncthreads();
+  if (grp > 0) return;
+  float top = -INFINITY, sum = 0.f, acc = 0.f;
+  for (int x = 0; x < 8; ++x) top = fmaxf(top, s_m[x]);
+  for (int x = 0; x < 8; ++x) {
+    const float w = s_m[x] == -INFINITY ? 0.f : exp2f(s_m[x] - top);
+    sum += w * s_l[x];
+    acc += w * s_o[x][d];
+  }
+  const int32_t bk = pair / p.hg, b = bk / p.Hkv;
+  const int32_t h = (bk % p.Hkv) * p.G + (pair % p.hg) * kDecodeGroup + head;
+  p.o[((int64_t)b * p.Hkv * p.G + h) * D + d] = __float2bfloat16_rn(acc / sum);
+  if (d == 0) p.lse[(int64_t)h * p.B + b] = 0.6931471805599453f * (top + log2f(sum));
 }
 
 }  // namespace segpaged

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/segpaged.h"
@@ -55,11 +56,52 @@ void launch_append(const AppendParams& p, cudaStream_t st) {
   append_kernel<D, FMT><<<(unsigned)ceil_div(lanes, 128), 128, 0, st>>>(p);
 }
 
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+constexpr size_t kMetaBytes = 2 * kDecodeMaxCtas * sizeof(int32_t);
+constexpr size_t kSlots = 2 * kDecodeMaxCtas;
+
+// A pool [pages][P][D] as boxes of `rows` rows x one column block, in the swizzle of the kernel's stages.
 template <int D, int FMT>
-int launch_decode(const DecodeParams& p, cudaStream_t st) {
-  const int64_t warps = (int64_t)p.B * p.Hkv * p.G;
-  decode_kernel<D, FMT><<<(unsigned)ceil_div(warps, 4), 128, 0, st>>>(p);
+bool encode_pool(CUtensorMap* map, const void* base, int P, int64_t pages) {
+  using C = DecodeCfg<D, FMT, 1>;
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * C::EB, (cuuint64_t)D * C::EB * P};
+  const cuuint32_t box[3] = {(cuuint32_t)(C::ROWB / C::EB), (cuuint32_t)std::min(P, 64), 1}, estr[3] = {1, 1, 1};
+  return enc(map, C::EB == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             C::ROWB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int FMT, int NB>
+int launch_decode_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int grid, cudaStream_t st) {
+  using C = DecodeCfg<D, FMT, NB>;
+  static std::atomic<bool> configured[kMaxDevices];  // per device; a race only repeats the call
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SEGPAGED_ERR_CUDA;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(decode_kernel<D, FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+        cudaSuccess)
+      return SEGPAGED_ERR_CUDA;
+    configured[dev].store(true, std::memory_order_release);
+  }
+  decode_kernel<D, FMT, NB><<<grid, kDecodeThreads, C::SMEM_BYTES, st>>>(tk, tv, p);
+  if (launched()) return SEGPAGED_ERR_CUDA;
+  decode_combine_kernel<D><<<dim3(grid, std::min(p.G, kDecodeGroup)), 8 * D, 0, st>>>(p);
   return launched();
+}
+
+// Up to eight query heads a KV head fill one column block of the products, up to sixteen two; larger groups take
+// several passes of sixteen.
+template <int D, int FMT>
+int launch_decode(const void* k_pool, const void* v_pool, const DecodeParams& p, int grid, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  if (!encode_pool<D, FMT>(&tk, k_pool, 1 << p.log2_page, p.num_pages) ||
+      !encode_pool<D, FMT>(&tv, v_pool, 1 << p.log2_page, p.num_pages))
+    return SEGPAGED_ERR_CUDA;
+  return p.G <= 8 ? launch_decode_nb<D, FMT, 1>(tk, tv, p, grid, st) : launch_decode_nb<D, FMT, 2>(tk, tv, p, grid, st);
 }
 
 }  // namespace
@@ -202,9 +244,10 @@ extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_form
   return launched();
 }
 
+// Per CTA the two chunks its run can start and end with, and which pair goes on behind it.
 extern "C" size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims) {
-  (void)dims;
-  return 256;
+  const size_t D = dims && dims->head_dim == 64 ? 64 : 128;
+  return align256(kMetaBytes) + align256(kSlots * kDecodeGroup * sizeof(float)) + kSlots * kDecodeGroup * D * sizeof(float);
 }
 
 extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format, const void* q, const void* k_pool,
@@ -220,10 +263,14 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   if (!q || (!page_table && page_table_len > 0) || !page_table_offs || !ctx_len || !cls || !o || !lse || !workspace) return SEGPAGED_ERR_NULL;
   if (workspace_bytes < segpaged_decode_workspace_bytes(dims)) return SEGPAGED_ERR_CAPACITY;
   if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return SEGPAGED_ERR_ALIGN;
+  const int sms = sm_count();
+  if (sms <= 0) return SEGPAGED_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_pool = static_cast<const uint8_t*>(k_pool);
-  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.part_meta = reinterpret_cast<int32_t*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + align256(kMetaBytes));
+  p.part_o = reinterpret_cast<float*>(ws + align256(kMetaBytes) + align256(kSlots * kDecodeGroup * sizeof(float)));
   p.kv_scale = kv_scale;
   p.table = page_table;
   p.offs = page_table_offs;
@@ -237,11 +284,12 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   p.B = dims->num_seqs;
   p.Hkv = dims->num_kv_heads;
   p.G = dims->num_q_heads / dims->num_kv_heads;
-  p.P = dims->page_size;
+  p.log2_page = log2_int(dims->page_size);
   p.num_pages = dims->num_pages;
+  p.hg = std::max(1, p.G / kDecodeGroup);
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = SEGPAGED_OK;
-  SEGPAGED_BY_SHAPE(rc = launch_decode, (p, st));
+  SEGPAGED_BY_SHAPE(rc = launch_decode, (k_pool, v_pool, p, std::min(sms, kDecodeMaxCtas), st));
   return rc;
 }
