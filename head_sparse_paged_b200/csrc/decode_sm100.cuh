@@ -38,7 +38,7 @@
 namespace segpaged {
 
 constexpr int kDecodeTile = 128;         // tokens of a tile
-constexpr int kDecodeWarps = 8;          // consumer warps, 16 tokens of a tile each
+constexpr int kDecodeWarps = 8;          // consumer warps
 constexpr int kDecodeThreads = 32 * (kDecodeWarps + 1);
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
@@ -66,6 +66,9 @@ struct DecodeParams {
 
 template <int D, int FMT, int NB>
 struct DecodeCfg {
+  // A warp takes 32 tokens of every second tile: two independent chains of products, and one maximum, wait and header
+  // for twice the tokens. With 16 heads the registers allow 16 tokens of every tile.
+  static constexpr int MB = NB == 1 ? 2 : 1;
   static constexpr int EB = FMT == kFmtBf16 ? 2 : 1;             // bytes of an element
   static constexpr int ROWB = D * EB < 128 ? D * EB : 128;       // bytes of a row in one column block
   static constexpr int CB = D * EB / ROWB;                       // column blocks
@@ -390,7 +393,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // ----------------------------------------------------------------------------------- consumers
     constexpr int KS = D / 16;  // k16 steps of a logit, and m16 tiles of O^T
     const int g = lane >> 2, t = lane & 3;
-    const int row0 = warp * 16;
+    constexpr int MB = C::MB, WPT = kDecodeWarps / MB;  // m16 blocks of a warp, warps of a tile
+    const int turn = warp / WPT;                        // which tiles, counted modulo MB, this warp takes part in
+    const int row0 = (warp % WPT) * 16 * MB;
     // ldmatrix row of this lane: rows 0-7 / 8-15 of the warp's tokens, chunk parity, for K (and bf16 / 8-bit V)
     const int lrow = row0 + (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
     const int trow = row0 + (lane & 7) + (lane >> 4) * 8, tchunk = (lane >> 3) & 1;  // bf16 V, transposed
@@ -461,64 +466,96 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           for (int mt = 0; mt < KS; ++mt) o[nb][mt][0] = o[nb][mt][1] = o[nb][mt][2] = o[nb][mt][3] = 0.f;
         }
       }
-      if (row0 + 16 > h.v0 && row0 < h.v1) {
-        const bool edge = row0 < h.v0 || row0 + 16 > h.v1;
-        // ---- logits: rows = tokens g, g + 8; columns = heads 2t, 2t + 1
-        float sc[NB][4];
+      if (i % MB == turn && row0 + 16 * MB > h.v0 && row0 < h.v1) {
+        const bool edge = row0 < h.v0 || row0 + 16 * MB > h.v1;
+        // ---- logits: rows = tokens g, g + 8 of each block; columns = heads 2t, 2t + 1
+        float sc[MB][NB][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) sc[mb][nb][0] = sc[mb][nb][1] = sc[mb][nb][2] = sc[mb][nb][3] = 0.f;
         if (BF) {
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            uint32_t a[4];
-            ldsm4(chunk_addr(kbase, lrow, 2 * ks + lchunk), a);
+          for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<true>(sc[nb], a[0], a[1], a[2], a[3], qf[nb][ks][0], qf[nb][ks][1]);
-          }
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < KS; ks += 2) {
-            uint32_t a[4];
-            ldsm4(chunk_addr(kbase, lrow, ks + lchunk), a);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t a0 = codes2<FMT>(a[2 * j]), a2 = codes2<FMT>(a[2 * j] >> 16);
-              const uint32_t a1 = codes2<FMT>(a[2 * j + 1]), a3 = codes2<FMT>(a[2 * j + 1] >> 16);
+            for (int mb = 0; mb < MB; ++mb) {
+              uint32_t a[4];
+              ldsm4(chunk_addr(kbase, lrow, 2 * ks + lchunk) + mb * 16 * C::ROWB, a);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
-                mma16816<false>(sc[nb], a0, a1, a2, a3, qf[nb][ks + j][0], qf[nb][ks + j][1]);
+                mma16816<true>(sc[mb][nb], a[0], a[1], a[2], a[3], qf[nb][ks][0], qf[nb][ks][1]);
+            }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ks += 2)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+              uint32_t a[4];
+              ldsm4(chunk_addr(kbase, lrow, ks + lchunk) + mb * 16 * C::ROWB, a);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t a0 = codes2<FMT>(a[2 * j]), a2 = codes2<FMT>(a[2 * j] >> 16);
+                const uint32_t a1 = codes2<FMT>(a[2 * j + 1]), a3 = codes2<FMT>(a[2 * j + 1] >> 16);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816<false>(sc[mb][nb], a0, a1, a2, a3, qf[nb][ks + j][0], qf[nb][ks + j][1]);
+              }
+            }
+        }
+        bool in[MB][2];
+        float kscale[MB][2], vscale[MB][2], vshift = 1.f;
+        int32_t vtop = 0;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const int r = row0 + 16 * mb + g;
+          in[mb][0] = r >= h.v0 && r < h.v1;
+          in[mb][1] = r + 8 >= h.v0 && r + 8 < h.v1;
+          if (!BF) {
+            const int page = 1 << p.log2_page;  // exponent bytes: [page of the tile][K, V][row]
+            const uint8_t* y = extra + ((r >> p.log2_page) << p.log2_page) * 2 + (r & (page - 1));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              kscale[mb][j] = row_scale(y[8 * j]);
+              const int32_t vy = y[page + 8 * j];
+              vscale[mb][j] = __int_as_float(vy);  // the byte, until the largest one is known
+              if (in[mb][j] && vy != kRowNaN) vtop = max(vtop, vy);
             }
           }
         }
-        const int r0 = row0 + g, r1 = r0 + 8;
-        const bool in0 = r0 >= h.v0 && r0 < h.v1, in1 = r1 >= h.v0 && r1 < h.v1;
-        float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f, vshift = 1.f;
         if (!BF) {
-          const int page = 1 << p.log2_page;  // exponent bytes: [page of the tile][K, V][row]
-          const int at = (row0 >> p.log2_page) * page * 2 + (row0 & (page - 1)) + g;
-          ks0 = row_scale(extra[at]);
-          ks1 = row_scale(extra[at + 8]);
-          const int32_t y0 = extra[at + page], y1 = extra[at + 8 + page];
-          int32_t top = max(in0 && y0 != kRowNaN ? y0 : 0, in1 && y1 != kRowNaN ? y1 : 0);
-          top = max(vref, __reduce_max_sync(0xffffffffu, top));
-          vshift = exp2_int(vref - top);
-          vref = top;
-          vs0 = y0 == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(y0 - top + 14);
-          vs1 = y1 == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(y1 - top + 14);
+          vtop = max(vref, __reduce_max_sync(0xffffffffu, vtop));
+          vshift = exp2_int(vref - vtop);
+          vref = vtop;
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int32_t vy = __float_as_int(vscale[mb][j]);
+              // a hidden token's byte may be anything: its weight is zero whatever that says
+              vscale[mb][j] = vy == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(vy - vtop + 14);
+              if (!in[mb][j]) vscale[mb][j] = 0.f;
+            }
         }
-        uint32_t pf[NB][2], pl[NB][2];
+        uint32_t pf[MB][NB][2], pl[MB][NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const float f0 = head_scale[nb][0], f1 = head_scale[nb][1];
-          float x0 = sc[nb][0] * (ks0 * f0), x1 = sc[nb][1] * (ks0 * f1);
-          float x2 = sc[nb][2] * (ks1 * f0), x3 = sc[nb][3] * (ks1 * f1);
-          if (edge) {
-            x0 = in0 ? x0 : -INFINITY;
-            x1 = in0 ? x1 : -INFINITY;
-            x2 = in1 ? x2 : -INFINITY;
-            x3 = in1 ? x3 : -INFINITY;
-          }
-          float n0 = fmaxf(x0, x2), n1 = fmaxf(x1, x3);
+          float n0 = -INFINITY, n1 = -INFINITY;
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float& x0 = sc[mb][nb][2 * j];
+              float& x1 = sc[mb][nb][2 * j + 1];
+              x0 *= BF ? f0 : kscale[mb][j] * f0;
+              x1 *= BF ? f1 : kscale[mb][j] * f1;
+              if (edge) {
+                x0 = in[mb][j] ? x0 : -INFINITY;
+                x1 = in[mb][j] ? x1 : -INFINITY;
+              }
+              n0 = fmaxf(n0, x0);
+              n1 = fmaxf(n1, x1);
+            }
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) {
             n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
@@ -545,68 +582,73 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             m[nb][1] = n1;
           }
           const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-          float p0 = ptx::ex2(x0 - b0), p1 = ptx::ex2(x1 - b1), p2 = ptx::ex2(x2 - b0), p3 = ptx::ex2(x3 - b1);
-          l[nb][0] += p0 + p2;
-          l[nb][1] += p1 + p3;
-          if (BF) {
-            const uint32_t h0 = ptx::pack_bf16x2(p0, p1), h1 = ptx::pack_bf16x2(p2, p3);
-            pf[nb][0] = transpose8x8(h0);
-            pf[nb][1] = transpose8x8(h1);
-            pl[nb][0] = transpose8x8(ptx::pack_bf16x2(p0 - bf16_lo(h0), p1 - bf16_hi(h0)));
-            pl[nb][1] = transpose8x8(ptx::pack_bf16x2(p2 - bf16_lo(h1), p3 - bf16_hi(h1)));
-          } else {
-            // a masked token's exponent byte may be anything: its weight is zero whatever that says
-            const float w0 = edge && !in0 ? 0.f : vs0, w1 = edge && !in1 ? 0.f : vs1;
-            pf[nb][0] = transpose8x8(pack_f16x2(p0 * w0, p1 * w0));
-            pf[nb][1] = transpose8x8(pack_f16x2(p2 * w1, p3 * w1));
-          }
-        }
-        // ---- O^T += V^T P^T. Rows outside [v0, v1) may hold NaN: their bits are cleared (tokens 2t, 2t+1 | +8)
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if (edge) {
-          auto halves = [&](int r) {
-            return (r >= h.v0 && r < h.v1 ? 0xffffu : 0u) | (r + 1 >= h.v0 && r + 1 < h.v1 ? 0xffff0000u : 0u);
-          };
-          keep0 = halves(row0 + 2 * t);
-          keep1 = halves(row0 + 2 * t + 8);
-        }
-        if (BF) {
 #pragma unroll
-          for (int mt = 0; mt < KS; ++mt) {
-            uint32_t a[4];
-            ldsm4_t(chunk_addr(vbase, trow, 2 * mt + tchunk), a);
-            if (edge) {
-              a[0] &= keep0;
-              a[1] &= keep0;
-              a[2] &= keep1;
-              a[3] &= keep1;
-            }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816<true>(o[nb][mt], a[0], a[1], a[2], a[3], pf[nb][0], pf[nb][1]);
-              mma16816<true>(o[nb][mt], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int mt = 0; mt < KS; mt += 2) {
-            uint32_t a[4];
-            ldsm4_t(chunk_addr(vbase, lrow, mt + lchunk), a);
+          for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              // bytes of a register: token 2t's codes of dims 2g, 2g+1, then token 2t+1's
-              const uint32_t x = __byte_perm(a[2 * j], 0, 0x3120), y = __byte_perm(a[2 * j + 1], 0, 0x3120);
-              uint32_t a0 = codes2<FMT>(x), a1 = codes2<FMT>(x >> 16), a2 = codes2<FMT>(y), a3 = codes2<FMT>(y >> 16);
+              const float p0 = ptx::ex2(sc[mb][nb][2 * j] - b0), p1 = ptx::ex2(sc[mb][nb][2 * j + 1] - b1);
+              l[nb][0] += p0;
+              l[nb][1] += p1;
+              if (BF) {
+                const uint32_t hi = ptx::pack_bf16x2(p0, p1);
+                pf[mb][nb][j] = transpose8x8(hi);
+                pl[mb][nb][j] = transpose8x8(ptx::pack_bf16x2(p0 - bf16_lo(hi), p1 - bf16_hi(hi)));
+              } else {
+                pf[mb][nb][j] = transpose8x8(pack_f16x2(p0 * vscale[mb][j], p1 * vscale[mb][j]));
+              }
+            }
+        }
+        // ---- O^T += V^T P^T. Rows outside [v0, v1) may hold NaN: their bits are cleared (tokens 2t, 2t+1 | +8)
+        uint32_t keep[MB][2];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = row0 + 16 * mb + 8 * j + 2 * t;
+            keep[mb][j] = (r >= h.v0 && r < h.v1 ? 0xffffu : 0u) | (r + 1 >= h.v0 && r + 1 < h.v1 ? 0xffff0000u : 0u);
+          }
+        if (BF) {
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+              uint32_t a[4];
+              ldsm4_t(chunk_addr(vbase, trow, 2 * mt + tchunk) + mb * 16 * C::ROWB, a);
               if (edge) {
-                a0 &= keep0;
-                a1 &= keep0;
-                a2 &= keep1;
-                a3 &= keep1;
+                a[0] &= keep[mb][0];
+                a[1] &= keep[mb][0];
+                a[2] &= keep[mb][1];
+                a[3] &= keep[mb][1];
               }
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma16816<false>(o[nb][mt + j], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
+              for (int nb = 0; nb < NB; ++nb) {
+                mma16816<true>(o[nb][mt], a[0], a[1], a[2], a[3], pf[mb][nb][0], pf[mb][nb][1]);
+                mma16816<true>(o[nb][mt], a[0], a[1], a[2], a[3], pl[mb][nb][0], pl[mb][nb][1]);
+              }
             }
-          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < KS; mt += 2)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+              uint32_t a[4];
+              ldsm4_t(chunk_addr(vbase, lrow, mt + lchunk) + mb * 16 * C::ROWB, a);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                // bytes of a register: token 2t's codes of dims 2g, 2g+1, then token 2t+1's
+                const uint32_t x = __byte_perm(a[2 * j], 0, 0x3120), y = __byte_perm(a[2 * j + 1], 0, 0x3120);
+                uint32_t a0 = codes2<FMT>(x), a1 = codes2<FMT>(x >> 16), a2 = codes2<FMT>(y), a3 = codes2<FMT>(y >> 16);
+                if (edge) {
+                  a0 &= keep[mb][0];
+                  a1 &= keep[mb][0];
+                  a2 &= keep[mb][1];
+                  a3 &= keep[mb][1];
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma16816<false>(o[nb][mt + j], a0, a1, a2, a3, pf[mb][nb][0], pf[mb][nb][1]);
+              }
+            }
         }
       }
       __syncwarp();
@@ -698,36 +740,46 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
 // Joins the chunks of the pairs that several CTAs shared: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
 // Block (c, head) does the pair whose first chunk CTA c left; its other chunks lie in the first slots of the CTAs
-// after it. Eight groups of D threads take every eighth chunk each and are merged in order.
+// after it. The warps take every kCombineWarps-th chunk each, a lane D/32 columns, and are merged in order.
+constexpr int kDecodeCombineWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(8 * D) decode_combine_kernel(const DecodeParams p) {
-  __shared__ float s_m[8], s_l[8], s_o[8][D];
+__global__ void __launch_bounds__(32 * kDecodeCombineWarps) decode_combine_kernel(const DecodeParams p) {
+  constexpr int E = D / 32;
+  __shared__ float s_m[kDecodeCombineWarps], s_l[kDecodeCombineWarps], s_o[kDecodeCombineWarps][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results of the launch before this one
   const int32_t cta = blockIdx.x, head = blockIdx.y;
   const int32_t pair = p.part_meta[2 * cta], n = p.part_meta[2 * cta + 1];
   if (n <= 1) return;
-  const int d = threadIdx.x % D, grp = threadIdx.x / D;
-  float m = -INFINITY, l = 0.f, o = 0.f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, o[E] = {};
 #pragma unroll 4
-  for (int32_t c = grp; c < n; c += 8) {
+  for (int32_t c = warp; c < n; c += kDecodeCombineWarps) {
     const int64_t at = (int64_t)(c == 0 ? 2 * cta + 1 : 2 * (cta + c)) * kDecodeGroup + head;
-    const float lc = p.part_lse[at], oc = p.part_o[at * D + d];
-    if (lc == -INFINITY) continue;
-    const float mn = fmaxf(m, lc), a = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(lc - mn);
+    const float lc = p.part_lse[at];
+    float oc[E];
+    if (E == 4) *reinterpret_cast<float4*>(oc) = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
+    else *reinterpret_cast<float2*>(oc) = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
+    const float mn = fmaxf(m, lc);
+    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - mn), w = lc == -INFINITY ? 0.f : ptx::ex2(lc - mn);
     l = l * a + w;
-    o = o * a + w * oc;
+#pragma unroll
+    for (int k = 0; k < E; ++k) o[k] = o[k] * a + (lc == -INFINITY ? 0.f : w * oc[k]);
     m = mn;
   }
-  s_o[grp][d] = o;
-  if (d == 0) {
-    s_m[grp] = m;
-    s_l[grp] = l;
+#pragma unroll
+  for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = o[k];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
   }
   __syncthreads();
-  if (grp > 0) return;
+  const int d = threadIdx.x;
+  if (d >= D) return;
   float top = -INFINITY, sum = 0.f, acc = 0.f;
-  for (int x = 0; x < 8; ++x) top = fmaxf(top, s_m[x]);
-  for (int x = 0; x < 8; ++x) {
-    const float w = s_m[x] == -INFINITY ? 0.f : exp2f(s_m[x] - top);
+  for (int x = 0; x < kDecodeCombineWarps; ++x) top = fmaxf(top, s_m[x]);
+  for (int x = 0; x < kDecodeCombineWarps; ++x) {
+    const float w = s_m[x] == -INFINITY ? 0.f : ptx::ex2(s_m[x] - top);
     sum += w * s_l[x];
     acc += w * s_o[x][d];
   }

@@ -89,7 +89,17 @@ int launch_decode_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeP
   }
   decode_kernel<D, FMT, NB><<<grid, kDecodeThreads, C::SMEM_BYTES, st>>>(tk, tv, p);
   if (launched()) return SEGPAGED_ERR_CUDA;
-  decode_combine_kernel<D><<<dim3(grid, std::min(p.G, kDecodeGroup)), 8 * D, 0, st>>>(p);
+  // Its blocks may start when the attention's last CTAs leave the SMs, and wait there for the whole grid.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, std::min(p.G, kDecodeGroup));
+  cfg.blockDim = dim3(32 * kDecodeCombineWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, decode_combine_kernel<D>, p) != cudaSuccess) return SEGPAGED_ERR_CUDA;
   return launched();
 }
 
