@@ -178,14 +178,6 @@ struct DecodeSmall {
 };
 static_assert(sizeof(DecodeSmall) <= 2048, "small shared arrays");
 
-// Producer's place in the list of tiles.
-struct DecodeCursor {
-  int32_t pair, tile, bk;
-  DecodeGeom g;
-  int64_t off, len;  // the head's page table: first entry, entries
-  int32_t n_sink, w0;
-};
-
 template <int D, int FMT, int NB>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const DecodeParams p) {
@@ -263,126 +255,154 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
   if (warp == kDecodeWarps) {
     // ------------------------------------------------------------------------------------ producer
+    // Works in batches of 32 boxes (a box: up to 64 rows of one page; 2 to 8 to a tile), one per lane: the lanes find
+    // their boxes' pages for the next batch, whose loads are then in flight while this batch's copies are issued.
+    // (Looking one tile ahead instead left 0.9 us per tile, the latency of a page id under load: 5.0 TB/s of an
+    // all-global layer's 2.2 GB.)
     const int32_t page = 1 << p.log2_page;
     const int32_t log2_box = min(p.log2_page, 6), box = 1 << log2_box;  // rows of one TMA box
-    const uint32_t boxes = kDecodeTile >> log2_box;
-    DecodeCursor c = {};
-    auto open_pair = [&](int32_t u) {
-      c.pair = u;
-      c.bk = u / p.hg;
-      c.g = decode_geom(p, c.bk);
-      const Split s = device_split(p.ctx_len, p.q_len, p.cls, c.bk / p.Hkv, c.bk, page, 1, &c.g.L);
-      c.off = p.offs[c.bk];
-      c.len = (int64_t)p.offs[c.bk + 1] - c.off;
-      c.n_sink = s.n_sink;
-      c.w0 = s.w0;
-      if (c.len != s.total && lane == 0) report(p.status, 2);
-    };
-    // First token of the cursor's tile and its visible tokens.
-    auto span = [&](int32_t& t0, int32_t& lo, int32_t& hi) {
-      const bool sink = c.tile < c.g.n_a;
-      t0 = sink ? c.tile * kDecodeTile : c.g.b0 + (c.tile - c.g.n_a) * kDecodeTile;
-      lo = max(t0, sink ? 0 : c.g.lo);
-      hi = (int32_t)min((int64_t)t0 + kDecodeTile, (int64_t)(sink ? c.g.a1 : c.g.L));
-    };
-    // Whether a visible token lies in this lane's box of the tile, and the page it is on (a load that nothing waits
-    // for before the page is used).
-    auto fetch = [&](bool& need) -> int32_t {
-      int32_t t0, lo, hi;
-      span(t0, lo, hi);
-      const int64_t tok = (int64_t)t0 + lane * box;
-      need = (uint32_t)lane < boxes && tok + box > lo && tok < hi;
-      if (!need) return 0;
-      const int32_t lp = (int32_t)(tok >> p.log2_page), t = lp < c.n_sink ? lp : lp - c.w0 + c.n_sink;
-      if (t >= c.len || c.off < 0 || c.off + t >= p.table_len) {
-        report(p.status, 2);
-        return 0;
+    const int32_t boxes = kDecodeTile >> log2_box, batch_tiles = 32 / boxes;
+    const int32_t my_tile = lane / boxes, my_row = (lane % boxes) * box;
+    // Window: lane k holds pair window + k, whose tiles are [w_end - w.n, w_end) of this CTA's run.
+    int32_t window = 0, w_end = 0, w_off = 0, w_len = 0, w_sink = 0, w_w0 = 0;
+    DecodeGeom w = {};
+    auto load_window = [&](int32_t u0, int32_t at) {  // `at`: where pair u0's tile 0 lies (negative: before the run)
+      window = u0;
+      w = DecodeGeom{};
+      if (u0 + lane < pairs) {
+        const int32_t bk = (u0 + lane) / p.hg;
+        w = decode_geom(p, bk);
+        int32_t L;
+        const Split s = device_split(p.ctx_len, p.q_len, p.cls, bk / p.Hkv, bk, page, 1, &L);
+        w_off = p.offs[bk];
+        w_len = p.offs[bk + 1] - w_off;
+        w_sink = s.n_sink;
+        w_w0 = s.w0;
+        if (w.n > 0 && w_len != s.total) report(p.status, 2);
       }
-      return __ldg(p.table + c.off + t);
+      w_end = w.n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, w_end, d);
+        if (lane >= d) w_end += x;
+      }
+      w_end += at;
+    };
+    struct Box {
+      int32_t id, row;  // page id as the table has it, first row in the page
+      bool need;        // a visible token lies in it
+      DecodeTileHeader h;
+    } cur, nxt;
+    // The boxes of tiles i0, i0 + 1, ... into nxt; returns how many tiles that are (0: the run is done).
+    auto plan = [&](int32_t i0) -> int32_t {
+      nxt.need = false;
+      if (i0 >= tiles) return 0;
+      int32_t stop = __shfl_sync(0xffffffffu, w_end, 31);
+      while (stop <= i0) {
+        if (window + 32 >= pairs) {  // only if the lengths changed while this call runs
+          sm.abort = 1;
+          return 0;
+        }
+        load_window(window + 32, stop);
+        stop = __shfl_sync(0xffffffffu, w_end, 31);
+      }
+      stop = min(stop, tiles);
+      const int32_t i = min(i0 + my_tile, stop - 1);
+      int32_t k = 0;  // pairs of the window that end at or before tile i
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+        if (__shfl_sync(0xffffffffu, w_end, k + d - 1) <= i) k += d;
+      const int32_t n = __shfl_sync(0xffffffffu, w.n, k), end_k = __shfl_sync(0xffffffffu, w_end, k);
+      const int32_t n_a = __shfl_sync(0xffffffffu, w.n_a, k), b0 = __shfl_sync(0xffffffffu, w.b0, k);
+      const int32_t a1 = __shfl_sync(0xffffffffu, w.a1, k), lo_k = __shfl_sync(0xffffffffu, w.lo, k);
+      const int32_t L = __shfl_sync(0xffffffffu, w.L, k), off = __shfl_sync(0xffffffffu, w_off, k);
+      const int32_t len = __shfl_sync(0xffffffffu, w_len, k), sink = __shfl_sync(0xffffffffu, w_sink, k);
+      const int32_t w0 = __shfl_sync(0xffffffffu, w_w0, k);
+      const int32_t tile = i - (end_k - n);
+      const bool in_sink = tile < n_a;
+      const int32_t t0 = in_sink ? tile * kDecodeTile : b0 + (tile - n_a) * kDecodeTile;
+      const int32_t lo = max(t0, in_sink ? 0 : lo_k);
+      const int32_t hi = (int32_t)min((int64_t)t0 + kDecodeTile, (int64_t)(in_sink ? a1 : L));
+      const bool last = i + 1 == tiles || tile + 1 == n;
+      nxt.h.v0 = lo - t0;
+      nxt.h.v1 = hi - t0;
+      nxt.h.pair = window + k;
+      nxt.h.flags = (tile == 0 || i == 0 ? 1 : 0) | (last ? 2 : 0);
+      const bool mine = i0 + my_tile < stop;
+      if (last) {
+        const bool from_start = tile <= i, to_end = tile + 1 == n;  // does the chunk hold the pair's first, last tile
+        if (!(from_start && to_end)) nxt.h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
+        if (mine && from_start && !to_end && my_row == 0) {
+          // the pair goes on in the CTAs after this one, to the CTA that holds its last tile
+          const long long end_tile = start + end_k;  // one past it, in the list of all tiles
+          p.part_meta[2 * cta] = window + k;
+          p.part_meta[2 * cta + 1] = (int32_t)((end_tile * ctas - 1) / total) - cta + 1;
+        }
+      }
+      const int64_t tok = (int64_t)t0 + my_row;
+      nxt.need = mine && my_tile < batch_tiles && tok + box > lo && tok < hi;
+      nxt.row = (int32_t)(tok & (page - 1));
+      nxt.id = 0;
+      if (nxt.need) {
+        const int32_t lp = (int32_t)(tok >> p.log2_page), t = lp < sink ? lp : lp - w0 + sink;
+        if (t >= len || off < 0 || (int64_t)off + t >= p.table_len) report(p.status, 2);
+        else nxt.id = __ldg(p.table + off + t);  // nothing waits for it before its batch is issued
+      }
+      return min(batch_tiles, stop - i0);
     };
     if (tiles > 0) {
-      open_pair(sm.pair0);
-      c.tile = sm.tile0;
-      bool need, first = true;
-      int32_t id = fetch(need);
+      load_window(sm.pair0, -sm.tile0);
+      int32_t i = 0, count = plan(0);
       uint32_t issued = 0;
-      for (int32_t i = 0; i < tiles; ++i) {
-        const int s = i % C::STAGES;
-        uint8_t* stage = ring + s * C::STAGE_BYTES;
-        uint8_t* extra = extras + s * C::EXTRA_BYTES;
-        int32_t t0, lo, hi;
-        span(t0, lo, hi);
-        const bool last = i + 1 == tiles || c.tile + 1 == c.g.n;
-        DecodeTileHeader h;
-        h.v0 = lo - t0;
-        h.v1 = hi - t0;
-        h.pair = c.pair;
-        h.flags = (first ? 1 : 0) | (last ? 2 : 0);
-        if (last) {
-          const bool from_start = c.tile <= i;  // the chunk holds the pair's tile 0
-          const bool to_end = c.tile + 1 == c.g.n;
-          if (!(from_start && to_end)) h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
-          if (from_start && !to_end && lane == 0) {
-            // the pair goes on in the CTAs after this one, to the CTA that holds its last tile
-            const long long end_tile = start + i - c.tile + c.g.n;  // one past it, in the list of all tiles
-            p.part_meta[2 * cta] = c.pair;
-            p.part_meta[2 * cta + 1] = (int32_t)((end_tile * ctas - 1) / total) - cta + 1;
-          }
-        }
-        int32_t pid = id;
-        const bool load = need;
-        // the next tile's page ids are on their way while this one waits for its stage
-        const int32_t this_bk = c.bk, this_pair = c.pair;
-        const bool this_first = first;
-        first = last;
-        if (i + 1 < tiles) {
-          if (++c.tile == c.g.n) {
-            int32_t u = c.pair + 1;
-            while (u < pairs && decode_geom(p, u / p.hg).n == 0) ++u;
-            if (u >= pairs) {  // only if the lengths changed while this call runs
-              sm.abort = 1;
-              break;
-            }
-            open_pair(u);
-            c.tile = 0;
-          }
-          id = fetch(need);
-        }
-        if (i >= C::STAGES && !warp_wait(&sm.empty[s], ((i / C::STAGES) - 1) & 1, &sm.abort, p.status))
-          break;
-        if (load && (uint32_t)pid >= (uint32_t)p.num_pages) {
+      bool ok = true;
+      while (count > 0 && ok) {
+        cur = nxt;
+        const int32_t next_count = plan(i + count);
+        if (cur.need && (uint32_t)cur.id >= (uint32_t)p.num_pages) {
           report(p.status, 1);
-          pid = 0;
+          cur.id = 0;
         }
-        const uint32_t have = __ballot_sync(0xffffffffu, load);
-        const uint32_t boxes_in_page = 1u << (p.log2_page - log2_box);
-        // one exponent copy per page: by the page's first box that is loaded
-        const uint32_t before_it = boxes_in_page == 1 ? 0u : ((1u << (lane & 1)) - 1u) << (lane & 30);
-        const bool scales = !BF && load && (have & before_it) == 0;
-        const uint32_t n_scales = BF ? 0 : __popc(__ballot_sync(0xffffffffu, scales));
-        if (lane == 0) {
-          sm.hdr[s] = h;
-          const uint32_t bytes = __popc(have) * 2 * box * D * C::EB + n_scales * 2 * page + (this_first ? heads * D * 2 : 0);
-          ptx::mbar_arrive_expect_tx(&sm.full[s], bytes);
-          if (this_first) {
-            const int32_t b = this_bk / p.Hkv, h0 = (this_bk % p.Hkv) * p.G + (this_pair % p.hg) * kDecodeGroup;
-            bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)b * Hq + h0) * D, heads * D * 2, &sm.full[s]);
+        for (int32_t j = 0; j < count; ++j, ++i) {
+          const int s = i % C::STAGES;
+          uint8_t* stage = ring + s * C::STAGE_BYTES;
+          uint8_t* extra = extras + s * C::EXTRA_BYTES;
+          if (i >= C::STAGES && !warp_wait(&sm.empty[s], ((i / C::STAGES) - 1) & 1, &sm.abort, p.status)) {
+            ok = false;
+            break;
           }
-        }
-        issued = i + 1;
-        __syncwarp();
-        if (load) {
-          const int32_t row = (int32_t)((t0 + lane * box) & (page - 1));
+          const bool load = my_tile == j && cur.need;
+          const uint32_t have = __ballot_sync(0xffffffffu, load);
+          // one copy of a page's exponent bytes: by the first of its boxes that is loaded
+          const uint32_t before_it = p.log2_page == log2_box ? 0u : ((1u << (lane & 1)) - 1u) << (lane & 30);
+          const bool scales = !BF && load && (have & before_it) == 0;
+          const uint32_t n_scales = BF ? 0 : __popc(__ballot_sync(0xffffffffu, scales));
+          if (lane == j * boxes) {
+            const bool with_q = cur.h.flags & 1;
+            sm.hdr[s] = cur.h;
+            ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + n_scales * 2 * page +
+                                                        (with_q ? heads * D * 2 : 0));
+            if (with_q) {
+              const int32_t bk = cur.h.pair / p.hg, b = bk / p.Hkv;
+              const int32_t h0 = (bk % p.Hkv) * p.G + (cur.h.pair % p.hg) * kDecodeGroup;
+              bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)b * Hq + h0) * D, heads * D * 2, &sm.full[s]);
+            }
+          }
+          issued = i + 1;
+          __syncwarp();
+          if (load) {
 #pragma unroll
-          for (int cb = 0; cb < C::CB; ++cb) {
-            const int at = cb * C::BLOCK_BYTES + lane * box * C::ROWB;
-            ptx::tma_load_3d(stage + at, &tk, cb * (C::ROWB / C::EB), row, pid, &sm.full[s]);
-            ptx::tma_load_3d(stage + C::TILE_BYTES + at, &tv, cb * (C::ROWB / C::EB), row, pid, &sm.full[s]);
+            for (int cb = 0; cb < C::CB; ++cb) {
+              const int at = cb * C::BLOCK_BYTES + my_row * C::ROWB;
+              ptx::tma_load_3d(stage + at, &tk, cb * (C::ROWB / C::EB), cur.row, cur.id, &sm.full[s]);
+              ptx::tma_load_3d(stage + C::TILE_BYTES + at, &tv, cb * (C::ROWB / C::EB), cur.row, cur.id, &sm.full[s]);
+            }
+            if (scales)
+              bulk_load(extra + ((my_row >> p.log2_page) << p.log2_page) * 2, p.kv_scale + (int64_t)cur.id * 2 * page,
+                        2 * page, &sm.full[s]);
           }
-          if (scales)
-            bulk_load(extra + (lane * box / page) * 2 * page, p.kv_scale + (int64_t)pid * 2 * page, 2 * page, &sm.full[s]);
+          __syncwarp();
         }
-        __syncwarp();
+        count = next_count;
       }
       // after a timeout: the copies in flight land before the block's memory is given up
       if (sm.abort)
