@@ -60,7 +60,7 @@ struct DecodeParams {
   int32_t* status;             // nullable
   int64_t table_len;
   int32_t B, Hkv, G, log2_page, num_pages;
-  int32_t hg;                  // passes of a group: max(1, G / 16)
+  int32_t log2_hg;             // passes of a group: max(1, G / 16)
   float scale_log2;
 };
 
@@ -78,18 +78,21 @@ struct DecodeCfg {
   static constexpr int Q_BYTES = NB * 8 * D * 2;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int EXTRA_BYTES = SCALE_BYTES + Q_BYTES;      // beside a stage: exponent bytes, query rows
-  static constexpr int MERGE_BYTES = kDecodeWarps / 2 * 8 * D * 4;
-  static constexpr int FIXED_BYTES = MERGE_BYTES + 2048 + 1024;  // + barriers and small arrays + alignment slack
+  static constexpr int FIXED_BYTES = 4096 + 1024;                // barriers and small arrays, alignment slack
   static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
   static_assert(STAGES >= 2, "ring");
+  static_assert(STAGE_BYTES >= kDecodeWarps * 8 * D * 4, "a stage holds the eight warps' O of one column block");
+  // What ending a chunk costs a CTA, in half tiles (about 1 us, against 1.6 us for a bf16 tile and 0.8 us for an 8-bit
+  // one of 128 columns).
+  static constexpr int PAIR_COST = FMT == kFmtBf16 ? 1 : 2;
 };
 
 // What a consumer needs to know of a tile.
 struct DecodeTileHeader {
-  int32_t v0, v1;   // visible rows [v0, v1) of the tile
-  int32_t pair;     // pair index (sequence, KV head, pass)
+  int32_t rows;     // visible rows [v0, v1) of the tile: v0 | v1 << 16
+  int32_t b, h0;    // sequence, first query head
   int32_t flags;    // bit 0: first tile of a chunk, bit 1: last; bits 2..: 1 + partial slot, 0: the whole pair
 };
 
@@ -97,20 +100,38 @@ struct DecodeTileHeader {
 struct DecodeGeom {
   int32_t L, a1, b0, lo, n_a, n;
 };
-
-__device__ __forceinline__ DecodeGeom decode_geom(const DecodeParams& p, int32_t bk) {
+// A pair: those tiles, the outputs they go to, and the page table: entries [off, off + len), logical page lp at entry lp
+// below n_sink and at lp - w0 + n_sink from there on.
+struct DecodePair {
   DecodeGeom g;
-  const int b = bk / p.Hkv;
-  g.L = max(p.ctx_len[b], 0);
-  const bool global = p.cls[3 * bk] != 0;
-  const int32_t sink = min(max(p.cls[3 * bk + 1], 0), g.L), win = max(p.cls[3 * bk + 2], 1);
-  g.lo = max(g.L - win, 0);
-  g.a1 = sink;
-  if (global || sink >= g.lo) g.a1 = g.lo = 0;  // one run of visible tokens
-  g.b0 = (g.lo >> p.log2_page) << p.log2_page;
-  g.n_a = (g.a1 + kDecodeTile - 1) / kDecodeTile;
-  g.n = g.n_a + (int32_t)(((int64_t)g.L - g.b0 + kDecodeTile - 1) / kDecodeTile);
-  return g;
+  int32_t off, len, n_sink, w0, b, h0;
+};
+
+// Pair u: (sequence, KV head, pass of 16 query heads), u = (b * Hkv + k) << log2_hg | pass. The page rule is
+// storage_split's, with shifts for its divisions: this runs at the start of every launch, before the first load.
+__device__ __forceinline__ DecodePair decode_pair(const DecodeParams& p, int32_t u) {
+  const int32_t bk = u >> p.log2_hg;
+  DecodePair r;
+  r.b = bk / p.Hkv;
+  r.h0 = (bk - r.b * p.Hkv) * p.G + (u - (bk << p.log2_hg)) * kDecodeGroup;
+  const int32_t L = max(p.ctx_len[r.b], 0), lq = max(p.q_len ? p.q_len[r.b] : 1, 1);
+  const int32_t global = p.cls[3 * bk], sink = min(max(p.cls[3 * bk + 1], 0), L), win = max(p.cls[3 * bk + 2], 1);
+  r.off = p.offs[bk];
+  r.len = p.offs[bk + 1] - r.off;
+  const int32_t lp = p.log2_page, last = (1 << lp) - 1;
+  r.g.L = L;
+  r.g.lo = max(L - win, 0);
+  r.g.a1 = sink;
+  if (global || sink >= r.g.lo) r.g.a1 = r.g.lo = 0;  // one run of visible tokens
+  r.g.b0 = (r.g.lo >> lp) << lp;
+  r.g.n_a = (r.g.a1 + kDecodeTile - 1) / kDecodeTile;
+  r.g.n = r.g.n_a + (int32_t)(((uint32_t)(L - r.g.b0) + kDecodeTile - 1) / kDecodeTile);
+  const int32_t n_all = (int32_t)(((uint32_t)L + last) >> lp);
+  r.n_sink = (int32_t)(((uint32_t)sink + last) >> lp);
+  r.w0 = (int32_t)(max((int64_t)L - lq - win + 1, (int64_t)0) >> lp);
+  if (global || r.w0 <= r.n_sink) r.n_sink = r.w0 = n_all;
+  if (r.g.n > 0 && r.len != r.n_sink + n_all - r.w0) report(p.status, 2);
+  return r;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -165,18 +186,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, status, kDecodeStatusTimeout));
 }
 
-// Shared memory beside the ring (2048 bytes).
+// Shared memory beside the ring (4096 bytes).
 struct DecodeSmall {
   uint64_t full[8], empty[8];
   uint64_t sync;                                // consumers' meeting point
   DecodeTileHeader hdr[8];
   float m[kDecodeWarps][16], l[kDecodeWarps][16];
   long long warp_sum[kDecodeWarps + 1];
-  long long start, total;                       // this CTA's first tile, tiles in all
+  long long first_rank, end_rank;               // this CTA's run in the list of all tiles
   int32_t pair0, tile0;                         // where its first tile lies
   int32_t abort;
+  DecodePair window[32];                        // pairs pair0 ..
 };
-static_assert(sizeof(DecodeSmall) <= 2048, "small shared arrays");
+static_assert(sizeof(DecodeSmall) <= 4096, "small shared arrays");
 
 template <int D, int FMT, int NB>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
@@ -186,11 +208,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* extras = ring + C::STAGES * C::STAGE_BYTES;
-  float* merge = reinterpret_cast<float*>(extras + C::STAGES * C::EXTRA_BYTES);
-  DecodeSmall& sm = *reinterpret_cast<DecodeSmall*>(extras + C::STAGES * C::EXTRA_BYTES + C::MERGE_BYTES);
+  DecodeSmall& sm = *reinterpret_cast<DecodeSmall*>(extras + C::STAGES * C::EXTRA_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t cta = blockIdx.x;
-  const int32_t pairs = p.B * p.Hkv * p.hg;
+  const int32_t pairs = (p.B * p.Hkv) << p.log2_hg;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -200,15 +221,27 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     ptx::mbar_init(&sm.sync, kDecodeWarps);
     ptx::mbar_fence_init();
     sm.abort = 0;
+    sm.first_rank = sm.end_rank = 0;
+    sm.pair0 = sm.tile0 = 0;
     ptx::tma_prefetch_desc(&tk);
     ptx::tma_prefetch_desc(&tv);
   }
+  // The launch may start while the one before it ends; nothing it wrote is read, and nothing written, before this.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's run of tiles: prefix sum over the pairs
+  // ---- this CTA's run of tiles. The work is counted in half tiles: a pair of n tiles is 2 n + PAIR_COST of them, and
+  // a CTA takes the tiles that begin in its equal share of the sum. Thread i adds up pairs [i * per, (i + 1) * per).
   const int32_t per = (pairs + kDecodeThreads - 1) / kDecodeThreads;
   const int32_t u_lo = min((int32_t)threadIdx.x * per, pairs), u_hi = min(u_lo + per, pairs);
+  DecodePair own = {};
   long long mine = 0;
-  for (int32_t u = u_lo; u < u_hi; ++u) mine += decode_geom(p, u / p.hg).n;
+  if (per == 1) {
+    if (u_lo < u_hi) own = decode_pair(p, u_lo);
+    mine = own.g.n;
+  } else {
+    for (int32_t u = u_lo; u < u_hi; ++u) mine += decode_pair(p, u).g.n;
+  }
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -218,40 +251,55 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   if (lane == 31) sm.warp_sum[warp] = incl;
   __syncthreads();
   long long before = incl - mine, total = 0;
+#pragma unroll
   for (int w = 0; w <= kDecodeWarps; ++w) {
-    if (w < warp) before += sm.warp_sum[w];
-    total += sm.warp_sum[w];
+    const long long x = sm.warp_sum[w];
+    if (w < warp) before += x;
+    total += x;
   }
-  const int32_t ctas = (int32_t)min((long long)gridDim.x, max(total, 1ll));  // each of these has a tile
-  const long long start = cta < ctas ? total * cta / ctas : total, end = cta < ctas ? total * (cta + 1) / ctas : total;
-  if (start < end && start >= before && start < before + mine) {
-    long long at = before;
+  const long long units = 2 * total + (long long)C::PAIR_COST * pairs;
+  // every CTA that takes part has two units or more, so one in the middle of a pair has a tile of it
+  const int32_t ctas = (int32_t)min((long long)gridDim.x, max(units / 2, 1ll));
+  const long long share = units <= 0xffffffffll ? (long long)((uint32_t)units / (uint32_t)ctas) : units / ctas;
+  const int32_t spare = (int32_t)(units - share * ctas);  // the first `spare` CTAs take one unit more
+  const long long lo_unit = cta < ctas ? share * cta + min(cta, spare) : units;
+  const long long hi_unit = cta < ctas ? lo_unit + share + (cta < spare) : units;
+  {
+    long long rank = before;
     for (int32_t u = u_lo; u < u_hi; ++u) {
-      const int32_t n = decode_geom(p, u / p.hg).n;
-      if (start < at + n) {
+      const int32_t n = per == 1 ? own.g.n : decode_pair(p, u).g.n;
+      const long long at = 2 * rank + (long long)C::PAIR_COST * u, next = at + 2 * n + C::PAIR_COST;
+      if (lo_unit >= at && lo_unit < next) {
         sm.pair0 = u;
-        sm.tile0 = (int32_t)(start - at);
-        break;
+        sm.tile0 = (int32_t)min((long long)n, (lo_unit - at + 1) / 2);
+        sm.first_rank = rank + sm.tile0;
       }
-      at += n;
+      if (hi_unit > at && hi_unit <= next) sm.end_rank = rank + min((long long)n, (hi_unit - at + 1) / 2);
+      rank += n;
     }
   }
   // pairs without a visible key (an empty sequence): O = 0, LSE = -inf, written by one CTA each
   const int32_t heads = min(p.G, kDecodeGroup), Hq = p.Hkv * p.G;
   for (int32_t u = u_lo; u < u_hi; ++u) {
-    const int32_t bk = u / p.hg, b = bk / p.Hkv;
-    if (u % (int32_t)gridDim.x != cta || p.ctx_len[b] > 0) continue;
-    const int32_t h0 = (bk % p.Hkv) * p.G + (u % p.hg) * kDecodeGroup;
-    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)b * Hq + h0) * D);
+    if (per == 1 ? own.g.n > 0 : p.ctx_len[(u >> p.log2_hg) / p.Hkv] > 0) continue;
+    if (u % (int32_t)gridDim.x != cta) continue;
+    const DecodePair e = decode_pair(p, u);
+    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)e.b * Hq + e.h0) * D);
     for (int i = 0; i < heads * D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
-    for (int h = 0; h < heads; ++h) p.lse[(int64_t)(h0 + h) * p.B + b] = -INFINITY;
+    for (int h = 0; h < heads; ++h) p.lse[(int64_t)(e.h0 + h) * p.B + e.b] = -INFINITY;
   }
   if (threadIdx.x == 0) {
     p.part_meta[2 * cta] = 0;
     p.part_meta[2 * cta + 1] = 0;
   }
   __syncthreads();
-  const int32_t tiles = (int32_t)(end - start);
+  const long long first_rank = sm.first_rank;
+  const int32_t tiles = cta < ctas ? (int32_t)max(sm.end_rank - first_rank, 0ll) : 0;
+  if (per == 1) {
+    const int32_t k = (int32_t)threadIdx.x - sm.pair0;
+    if (k >= 0 && k < 32) sm.window[k] = own;
+    __syncthreads();
+  }
 
   if (warp == kDecodeWarps) {
     // ------------------------------------------------------------------------------------ producer
@@ -263,24 +311,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int32_t log2_box = min(p.log2_page, 6), box = 1 << log2_box;  // rows of one TMA box
     const int32_t boxes = kDecodeTile >> log2_box, batch_tiles = 32 / boxes;
     const int32_t my_tile = lane / boxes, my_row = (lane % boxes) * box;
-    // Window: lane k holds pair window + k, whose tiles are [w_end - w.n, w_end) of this CTA's run.
-    int32_t window = 0, w_end = 0, w_off = 0, w_len = 0, w_sink = 0, w_w0 = 0;
-    DecodeGeom w = {};
-    auto load_window = [&](int32_t u0, int32_t at) {  // `at`: where pair u0's tile 0 lies (negative: before the run)
+    // Window: lane k holds pair window + k, whose tiles are [w_end - w.g.n, w_end) of this CTA's run.
+    int32_t window = 0, w_end = 0;
+    DecodePair w = {};
+    auto load_window = [&](int32_t u0, int32_t at, bool cached) {  // `at`: where pair u0's tile 0 lies in the run
       window = u0;
-      w = DecodeGeom{};
-      if (u0 + lane < pairs) {
-        const int32_t bk = (u0 + lane) / p.hg;
-        w = decode_geom(p, bk);
-        int32_t L;
-        const Split s = device_split(p.ctx_len, p.q_len, p.cls, bk / p.Hkv, bk, page, 1, &L);
-        w_off = p.offs[bk];
-        w_len = p.offs[bk + 1] - w_off;
-        w_sink = s.n_sink;
-        w_w0 = s.w0;
-        if (w.n > 0 && w_len != s.total) report(p.status, 2);
-      }
-      w_end = w.n;
+      w = DecodePair{};
+      if (u0 + lane < pairs) w = cached ? sm.window[lane] : decode_pair(p, u0 + lane);
+      w_end = w.g.n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int32_t x = __shfl_up_sync(0xffffffffu, w_end, d);
@@ -303,7 +341,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           sm.abort = 1;
           return 0;
         }
-        load_window(window + 32, stop);
+        load_window(window + 32, stop, false);
         stop = __shfl_sync(0xffffffffu, w_end, 31);
       }
       stop = min(stop, tiles);
@@ -312,21 +350,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1)
         if (__shfl_sync(0xffffffffu, w_end, k + d - 1) <= i) k += d;
-      const int32_t n = __shfl_sync(0xffffffffu, w.n, k), end_k = __shfl_sync(0xffffffffu, w_end, k);
-      const int32_t n_a = __shfl_sync(0xffffffffu, w.n_a, k), b0 = __shfl_sync(0xffffffffu, w.b0, k);
-      const int32_t a1 = __shfl_sync(0xffffffffu, w.a1, k), lo_k = __shfl_sync(0xffffffffu, w.lo, k);
-      const int32_t L = __shfl_sync(0xffffffffu, w.L, k), off = __shfl_sync(0xffffffffu, w_off, k);
-      const int32_t len = __shfl_sync(0xffffffffu, w_len, k), sink = __shfl_sync(0xffffffffu, w_sink, k);
-      const int32_t w0 = __shfl_sync(0xffffffffu, w_w0, k);
+      const int32_t n = __shfl_sync(0xffffffffu, w.g.n, k), end_k = __shfl_sync(0xffffffffu, w_end, k);
+      const int32_t n_a = __shfl_sync(0xffffffffu, w.g.n_a, k), b0 = __shfl_sync(0xffffffffu, w.g.b0, k);
+      const int32_t a1 = __shfl_sync(0xffffffffu, w.g.a1, k), lo_k = __shfl_sync(0xffffffffu, w.g.lo, k);
+      const int32_t L = __shfl_sync(0xffffffffu, w.g.L, k), off = __shfl_sync(0xffffffffu, w.off, k);
+      const int32_t len = __shfl_sync(0xffffffffu, w.len, k), sink = __shfl_sync(0xffffffffu, w.n_sink, k);
+      const int32_t w0 = __shfl_sync(0xffffffffu, w.w0, k);
       const int32_t tile = i - (end_k - n);
       const bool in_sink = tile < n_a;
       const int32_t t0 = in_sink ? tile * kDecodeTile : b0 + (tile - n_a) * kDecodeTile;
       const int32_t lo = max(t0, in_sink ? 0 : lo_k);
       const int32_t hi = (int32_t)min((int64_t)t0 + kDecodeTile, (int64_t)(in_sink ? a1 : L));
       const bool last = i + 1 == tiles || tile + 1 == n;
-      nxt.h.v0 = lo - t0;
-      nxt.h.v1 = hi - t0;
-      nxt.h.pair = window + k;
+      nxt.h.rows = (lo - t0) | (hi - t0) << 16;
+      nxt.h.b = __shfl_sync(0xffffffffu, w.b, k);
+      nxt.h.h0 = __shfl_sync(0xffffffffu, w.h0, k);
       nxt.h.flags = (tile == 0 || i == 0 ? 1 : 0) | (last ? 2 : 0);
       const bool mine = i0 + my_tile < stop;
       if (last) {
@@ -334,9 +372,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (!(from_start && to_end)) nxt.h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
         if (mine && from_start && !to_end && my_row == 0) {
           // the pair goes on in the CTAs after this one, to the CTA that holds its last tile
-          const long long end_tile = start + end_k;  // one past it, in the list of all tiles
+          const long long at = 2 * (first_rank + end_k - 1) + (long long)C::PAIR_COST * (window + k);  // its unit
+          const long long wide = (share + 1) * spare;  // units of the CTAs that take one more
+          const int32_t to = at < wide ? (int32_t)(at / (share + 1)) : spare + (int32_t)((at - wide) / share);
           p.part_meta[2 * cta] = window + k;
-          p.part_meta[2 * cta + 1] = (int32_t)((end_tile * ctas - 1) / total) - cta + 1;
+          p.part_meta[2 * cta + 1] = to - cta + 1;
         }
       }
       const int64_t tok = (int64_t)t0 + my_row;
@@ -351,7 +391,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       return min(batch_tiles, stop - i0);
     };
     if (tiles > 0) {
-      load_window(sm.pair0, -sm.tile0);
+      load_window(sm.pair0, -sm.tile0, per == 1);
       int32_t i = 0, count = plan(0);
       uint32_t issued = 0;
       bool ok = true;
@@ -382,9 +422,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + n_scales * 2 * page +
                                                         (with_q ? heads * D * 2 : 0));
             if (with_q) {
-              const int32_t bk = cur.h.pair / p.hg, b = bk / p.Hkv;
-              const int32_t h0 = (bk % p.Hkv) * p.G + (cur.h.pair % p.hg) * kDecodeGroup;
-              bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)b * Hq + h0) * D, heads * D * 2, &sm.full[s]);
+              bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)cur.h.b * Hq + cur.h.h0) * D, heads * D * 2, &sm.full[s]);
             }
           }
           issued = i + 1;
@@ -440,6 +478,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const int s = i % C::STAGES;
       if (!warp_wait(&sm.full[s], (i / C::STAGES) & 1, &sm.abort, p.status)) break;
       const DecodeTileHeader h = sm.hdr[s];
+      const int32_t v0 = h.rows & 0xffff, v1 = h.rows >> 16;
       const uint32_t kbase = ptx::smem_addr(ring + s * C::STAGE_BYTES), vbase = kbase + C::TILE_BYTES;
       const uint8_t* extra = extras + s * C::EXTRA_BYTES;
       if (h.flags & 1) {
@@ -486,8 +525,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           for (int mt = 0; mt < KS; ++mt) o[nb][mt][0] = o[nb][mt][1] = o[nb][mt][2] = o[nb][mt][3] = 0.f;
         }
       }
-      if (i % MB == turn && row0 + 16 * MB > h.v0 && row0 < h.v1) {
-        const bool edge = row0 < h.v0 || row0 + 16 * MB > h.v1;
+      if (i % MB == turn && row0 + 16 * MB > v0 && row0 < v1) {
+        const bool edge = row0 < v0 || row0 + 16 * MB > v1;
         // ---- logits: rows = tokens g, g + 8 of each block; columns = heads 2t, 2t + 1
         float sc[MB][NB][4];
 #pragma unroll
@@ -528,8 +567,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
           const int r = row0 + 16 * mb + g;
-          in[mb][0] = r >= h.v0 && r < h.v1;
-          in[mb][1] = r + 8 >= h.v0 && r + 8 < h.v1;
+          in[mb][0] = r >= v0 && r < v1;
+          in[mb][1] = r + 8 >= v0 && r + 8 < v1;
           if (!BF) {
             const int page = 1 << p.log2_page;  // exponent bytes: [page of the tile][K, V][row]
             const uint8_t* y = extra + ((r >> p.log2_page) << p.log2_page) * 2 + (r & (page - 1));
@@ -625,7 +664,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int r = row0 + 16 * mb + 8 * j + 2 * t;
-            keep[mb][j] = (r >= h.v0 && r < h.v1 ? 0xffffu : 0u) | (r + 1 >= h.v0 && r + 1 < h.v1 ? 0xffff0000u : 0u);
+            keep[mb][j] = (r >= v0 && r < v1 ? 0xffffu : 0u) | (r + 1 >= v0 && r + 1 < v1 ? 0xffff0000u : 0u);
           }
         if (BF) {
 #pragma unroll
@@ -671,14 +710,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             }
         }
       }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);  // this warp has read its rows
-      if (!(h.flags & 2)) continue;
+      if (!(h.flags & 2)) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);  // this warp has read its rows
+        continue;
+      }
 
-      // ---- a chunk ends: the eight warps' results become one
-      const int32_t bk = h.pair / p.hg, b = bk / p.Hkv;
-      const int32_t h0 = (bk % p.Hkv) * p.G + (h.pair % p.hg) * kDecodeGroup;
-      const int32_t slot = (h.flags >> 2) - 1;
+      // ---- a chunk ends: the eight warps' results become one, through the stage of its last tile
+      const int32_t b = h.b, h0 = h.h0, slot = (h.flags >> 2) - 1;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -690,43 +729,45 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             sm.l[warp][nb * 8 + 2 * t + j] = l[nb][j];
           }
         }
-      if (!meet()) break;
+      if (!meet()) break;  // from here no warp reads the tile any more
+      float* scratch = reinterpret_cast<float*>(ring + s * C::STAGE_BYTES);  // [warp][KS * 4][lane]
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
+        const bool live = nb * 8 + 2 * t < heads;  // this lane's columns are heads of the group
         float top[2], sum[2], w[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int head = nb * 8 + 2 * t + j;
+          float ms[kDecodeWarps];
           top[j] = -INFINITY;
-          for (int x = 0; x < kDecodeWarps; ++x) top[j] = fmaxf(top[j], sm.m[x][head]);
-          sum[j] = 0.f;
+#pragma unroll
           for (int x = 0; x < kDecodeWarps; ++x) {
-            const float mx = sm.m[x][head];
-            sum[j] += (mx == -INFINITY ? 0.f : ptx::ex2(mx - top[j])) * sm.l[x][head];
+            ms[x] = sm.m[x][head];
+            top[j] = fmaxf(top[j], ms[x]);
           }
+          sum[j] = 0.f;
+#pragma unroll
+          for (int x = 0; x < kDecodeWarps; ++x)
+            sum[j] += (ms[x] == -INFINITY ? 0.f : ptx::ex2(ms[x] - top[j])) * sm.l[x][head];
           w[j] = m[nb][j] == -INFINITY ? 0.f : ptx::ex2(m[nb][j] - top[j]);
           if (!BF) w[j] *= exp2_int(vref - 127 - 14);
         }
-        float* mine_m = merge + (warp & 3) * (KS * 128) + lane;
-        if (warp >= 4)
+        if (live)
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mine_m[(mt * 4 + c) * 32] = o[nb][mt][c] * w[c & 1];
-        if (!meet()) break;
-        if (warp < 4)
-#pragma unroll
-          for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) mine_m[(mt * 4 + c) * 32] += o[nb][mt][c] * w[c & 1];
+            for (int c = 0; c < 4; ++c) scratch[((warp * KS + mt) * 4 + c) * 32 + lane] = o[nb][mt][c] * w[c & 1];
         if (!meet()) break;
         // warp x finishes the 16 dims of m-tile x; this lane's heads are again 2t, 2t + 1
-        if (warp < KS) {
+        if (warp < KS && live) {
           float v[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float* from = merge + (warp * 4 + c) * 32 + lane;
-            v[c] = (from[0] + from[KS * 128]) + (from[2 * KS * 128] + from[3 * KS * 128]);
+            const float* from = scratch + (warp * 4 + c) * 32 + lane;
+            float part[kDecodeWarps];
+#pragma unroll
+            for (int x = 0; x < kDecodeWarps; ++x) part[x] = from[x * KS * 128];
+            v[c] = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
           }
           const int d0 = 16 * warp + (BF ? g : 2 * g), d1 = d0 + (BF ? 8 : 1);
 #pragma unroll
@@ -750,9 +791,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             }
           }
         }
-        if (nb + 1 < NB && !meet()) break;  // the buffer is free again
+        if (nb + 1 < NB && !meet()) break;  // the scratch is free again
       }
-      if (ok) meet();  // as are the buffer and sm.m, sm.l for the next chunk
+      ptx::fence_proxy_async_smem();  // the scratch was written by plain stores; the next writer is a TMA copy
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
     }
   }
   __syncthreads();
@@ -765,46 +808,71 @@ constexpr int kDecodeCombineWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kDecodeCombineWarps) decode_combine_kernel(const DecodeParams p) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[kDecodeCombineWarps], s_l[kDecodeCombineWarps], s_o[kDecodeCombineWarps][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results of the launch before this one
+  constexpr int E = D / 32, NW = kDecodeCombineWarps;
+  constexpr int U = kDecodeMaxCtas / NW / 2;  // chunks of a warp whose loads are issued together
+  __shared__ float s_lse[kDecodeMaxCtas], s_sum[NW], s_top[NW], s_o[NW][D];
   const int32_t cta = blockIdx.x, head = blockIdx.y;
-  const int32_t pair = p.part_meta[2 * cta], n = p.part_meta[2 * cta + 1];
-  if (n <= 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.f, o[E] = {};
-#pragma unroll 4
-  for (int32_t c = warp; c < n; c += kDecodeCombineWarps) {
-    const int64_t at = (int64_t)(c == 0 ? 2 * cta + 1 : 2 * (cta + c)) * kDecodeGroup + head;
-    const float lc = p.part_lse[at];
-    float oc[E];
-    if (E == 4) *reinterpret_cast<float4*>(oc) = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
-    else *reinterpret_cast<float2*>(oc) = reinterpret_cast<const float2*>(p.part_o + at * D)[lane];
-    const float mn = fmaxf(m, lc);
-    const float a = m == -INFINITY ? 0.f : ptx::ex2(m - mn), w = lc == -INFINITY ? 0.f : ptx::ex2(lc - mn);
-    l = l * a + w;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results of the launch before this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int32_t pair = p.part_meta[2 * cta], n = min(p.part_meta[2 * cta + 1], kDecodeMaxCtas);
+  if (n <= 1) return;
+  auto slot = [&](int32_t c) { return (int64_t)(c == 0 ? 2 * cta + 1 : 2 * (cta + c)) * kDecodeGroup + head; };
+  // log2 sums: their maximum, and the sum of the weights 2^(lse - maximum)
+  float top = -INFINITY;
+  for (int32_t c = threadIdx.x; c < n; c += 32 * NW) {
+    const float x = p.part_lse[slot(c)];
+    s_lse[c] = x;
+    top = fmaxf(top, x);
+  }
+  float o[E] = {};
+  float v[U][E];
+  auto load = [&](int32_t c0) {
 #pragma unroll
-    for (int k = 0; k < E; ++k) o[k] = o[k] * a + (lc == -INFINITY ? 0.f : w * oc[k]);
-    m = mn;
+    for (int u = 0; u < U; ++u) {
+      const int32_t c = c0 + u * NW;
+      if (c >= n) continue;
+      const float* from = p.part_o + slot(c) * D + lane * E;
+      if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(from);
+      else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(from);
+    }
+  };
+  load(warp);  // on its way while the weights are worked out
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < NW; ++x) top = fmaxf(top, s_top[x]);
+  auto weight = [&](int32_t c) { return s_lse[c] == -INFINITY ? 0.f : ptx::ex2(s_lse[c] - top); };
+  float sum = 0.f;
+  for (int32_t c0 = warp; c0 < n; c0 += U * NW) {
+    if (c0 != warp) load(c0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t c = c0 + u * NW;
+      if (c >= n) continue;
+      const float w = weight(c);
+      sum += w;
+#pragma unroll
+      for (int k = 0; k < E; ++k) o[k] += w == 0.f ? 0.f : w * v[u][k];
+    }
   }
 #pragma unroll
   for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = o[k];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+  if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
   const int d = threadIdx.x;
   if (d >= D) return;
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
-  for (int x = 0; x < kDecodeCombineWarps; ++x) top = fmaxf(top, s_m[x]);
-  for (int x = 0; x < kDecodeCombineWarps; ++x) {
-    const float w = s_m[x] == -INFINITY ? 0.f : ptx::ex2(s_m[x] - top);
-    sum += w * s_l[x];
-    acc += w * s_o[x][d];
+  float acc = 0.f;
+  sum = 0.f;
+#pragma unroll
+  for (int x = 0; x < NW; ++x) {
+    acc += s_o[x][d];
+    sum += s_sum[x];
   }
-  const int32_t bk = pair / p.hg, b = bk / p.Hkv;
-  const int32_t h = (bk % p.Hkv) * p.G + (pair % p.hg) * kDecodeGroup + head;
+  const int32_t bk = pair >> p.log2_hg, b = bk / p.Hkv;
+  const int32_t h = (bk - b * p.Hkv) * p.G + (pair - (bk << p.log2_hg)) * kDecodeGroup + head;
   p.o[((int64_t)b * p.Hkv * p.G + h) * D + d] = __float2bfloat16_rn(acc / sum);
   if (d == 0) p.lse[(int64_t)h * p.B + b] = 0.6931471805599453f * (top + log2f(sum));
 }

@@ -87,18 +87,22 @@ int launch_decode_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeP
       return SEGPAGED_ERR_CUDA;
     configured[dev].store(true, std::memory_order_release);
   }
-  decode_kernel<D, FMT, NB><<<grid, kDecodeThreads, C::SMEM_BYTES, st>>>(tk, tv, p);
-  if (launched()) return SEGPAGED_ERR_CUDA;
-  // Its blocks may start when the attention's last CTAs leave the SMs, and wait there for the whole grid.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, std::min(p.G, kDecodeGroup));
-  cfg.blockDim = dim3(32 * kDecodeCombineWarps);
-  cfg.stream = st;
+  // Both launches may start while the work before them ends (each waits for that before it reads or writes anything):
+  // their set-up overlaps its last blocks.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kDecodeThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, decode_kernel<D, FMT, NB>, tk, tv, p) != cudaSuccess) return SEGPAGED_ERR_CUDA;
+  cfg.gridDim = dim3(grid, std::min(p.G, kDecodeGroup));
+  cfg.blockDim = dim3(32 * kDecodeCombineWarps);
+  cfg.dynamicSmemBytes = 0;
   if (cudaLaunchKernelEx(&cfg, decode_combine_kernel<D>, p) != cudaSuccess) return SEGPAGED_ERR_CUDA;
   return launched();
 }
@@ -296,7 +300,7 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   p.G = dims->num_q_heads / dims->num_kv_heads;
   p.log2_page = log2_int(dims->page_size);
   p.num_pages = dims->num_pages;
-  p.hg = std::max(1, p.G / kDecodeGroup);
+  p.log2_hg = p.G > kDecodeGroup ? log2_int(p.G / kDecodeGroup) : 0;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = SEGPAGED_OK;
