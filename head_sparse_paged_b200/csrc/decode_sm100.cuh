@@ -38,8 +38,7 @@
 namespace segpaged {
 
 constexpr int kDecodeTile = 128;         // tokens of a tile
-constexpr int kDecodeWarps = 8;          // consumer warps
-constexpr int kDecodeThreads = 32 * (kDecodeWarps + 1);
+constexpr int kDecodeMaxWarps = 12;      // most consumer warps
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
 constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
@@ -69,6 +68,10 @@ struct DecodeCfg {
   // A warp takes 32 tokens of every second tile: two independent chains of products, and one maximum, wait and header
   // for twice the tokens. With 16 heads the registers allow 16 tokens of every tile.
   static constexpr int MB = NB == 1 ? 2 : 1;
+  static constexpr int WARPS = NB == 1 && FMT != kFmtBf16 ? 12 : 8;               // consumer warps
+  static constexpr int TILE_WARPS = kDecodeTile / (16 * MB);     // of which these share a tile
+  static constexpr int TURNS = WARPS / TILE_WARPS;
+  static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int EB = FMT == kFmtBf16 ? 2 : 1;             // bytes of an element
   static constexpr int ROWB = D * EB < 128 ? D * EB : 128;       // bytes of a row in one column block
   static constexpr int CB = D * EB / ROWB;                       // column blocks
@@ -83,10 +86,15 @@ struct DecodeCfg {
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
   static_assert(STAGES >= 2, "ring");
-  static_assert(STAGE_BYTES >= kDecodeWarps * 8 * D * 4, "a stage holds the eight warps' O of one column block");
+  static_assert(STAGE_BYTES >= 8 * 8 * D * 4, "a stage holds eight warps' O of one column block");
   // What ending a chunk costs a CTA, in half tiles (about 1 us, against 1.6 us for a bf16 tile and 0.8 us for an 8-bit
   // one of 128 columns).
   static constexpr int PAIR_COST = FMT == kFmtBf16 ? 1 : 2;
+};
+
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
 };
 
 // What a consumer needs to know of a tile.
@@ -161,11 +169,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-template <int FMT>
-__device__ __forceinline__ uint32_t codes2(uint32_t w) {
-  const __half2 h = codes_to_half2<FMT>(w);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -191,8 +194,8 @@ struct DecodeSmall {
   uint64_t full[8], empty[8];
   uint64_t sync;                                // consumers' meeting point
   DecodeTileHeader hdr[8];
-  float m[kDecodeWarps][16], l[kDecodeWarps][16];
-  long long warp_sum[kDecodeWarps + 1];
+  float m[kDecodeMaxWarps][16], l[kDecodeMaxWarps][16];
+  long long warp_sum[kDecodeMaxWarps + 1];
   long long first_rank, end_rank;               // this CTA's run in the list of all tiles
   int32_t pair0, tile0;                         // where its first tile lies
   int32_t abort;
@@ -201,7 +204,7 @@ struct DecodeSmall {
 static_assert(sizeof(DecodeSmall) <= 4096, "small shared arrays");
 
 template <int D, int FMT, int NB>
-__global__ void __launch_bounds__(kDecodeThreads, 1)
+__global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const DecodeParams p) {
   using C = DecodeCfg<D, FMT, NB>;
   constexpr bool BF = FMT == kFmtBf16;
@@ -216,9 +219,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       ptx::mbar_init(&sm.full[s], 1);
-      ptx::mbar_init(&sm.empty[s], kDecodeWarps);
+      ptx::mbar_init(&sm.empty[s], C::WARPS);
     }
-    ptx::mbar_init(&sm.sync, kDecodeWarps);
+    ptx::mbar_init(&sm.sync, C::WARPS);
     ptx::mbar_fence_init();
     sm.abort = 0;
     sm.first_rank = sm.end_rank = 0;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
   // ---- this CTA's run of tiles. The work is counted in half tiles: a pair of n tiles is 2 n + PAIR_COST of them, and
   // a CTA takes the tiles that begin in its equal share of the sum. Thread i adds up pairs [i * per, (i + 1) * per).
-  const int32_t per = (pairs + kDecodeThreads - 1) / kDecodeThreads;
+  const int32_t per = (pairs + C::THREADS - 1) / C::THREADS;
   const int32_t u_lo = min((int32_t)threadIdx.x * per, pairs), u_hi = min(u_lo + per, pairs);
   DecodePair own = {};
   long long mine = 0;
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w <= kDecodeWarps; ++w) {
+  for (int w = 0; w <= C::WARPS; ++w) {
     const long long x = sm.warp_sum[w];
     if (w < warp) before += x;
     total += x;
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     __syncthreads();
   }
 
-  if (warp == kDecodeWarps) {
+  if (warp == C::WARPS) {
     // ------------------------------------------------------------------------------------ producer
     // Works in batches of 32 boxes (a box: up to 64 rows of one page; 2 to 8 to a tile), one per lane: the lanes find
     // their boxes' pages for the next batch, whose loads are then in flight while this batch's copies are issued.
@@ -451,16 +454,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // ----------------------------------------------------------------------------------- consumers
     constexpr int KS = D / 16;  // k16 steps of a logit, and m16 tiles of O^T
     const int g = lane >> 2, t = lane & 3;
-    constexpr int MB = C::MB, WPT = kDecodeWarps / MB;  // m16 blocks of a warp, warps of a tile
-    const int turn = warp / WPT;                        // which tiles, counted modulo MB, this warp takes part in
-    const int row0 = (warp % WPT) * 16 * MB;
-    // ldmatrix row of this lane: rows 0-7 / 8-15 of the warp's tokens, chunk parity, for K (and bf16 / 8-bit V)
-    const int lrow = row0 + (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
-    const int trow = row0 + (lane & 7) + (lane >> 4) * 8, tchunk = (lane >> 3) & 1;  // bf16 V, transposed
-    auto chunk_addr = [](uint32_t base, int row, int chunk) {  // 16-byte chunk of a row in the swizzled tile
-      if (C::ROWB == 128)
-        return base + (chunk >> 3) * C::BLOCK_BYTES + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-      return base + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+    constexpr int MB = C::MB;
+    const int turn = warp / C::TILE_WARPS;  // which tiles, counted modulo TURNS, this warp takes part in
+    const int row0 = (warp % C::TILE_WARPS) * 16 * MB;
+    // ldmatrix row of this lane in a block of 16 tokens, and its 16-byte chunk (0 or 1 of a pair). The swizzle XORs a
+    // few row bits into the chunk bits of the address, so chunk c of the row is at (address of chunk 0) ^ (c << 4).
+    const int lrow = row0 + (lane & 15), lchunk = lane >> 4;                                   // K, and 8-bit V
+    const int trow = row0 + (lane & 7) + (lane >> 4) * 8, tchunk = (lane >> 3) & 1;            // bf16 V
+    auto lane_base = [](int row, int chunk) {
+      return C::ROWB == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+    };
+    const uint32_t k_lane = lane_base(lrow, lchunk);
+    const uint32_t v_lane = C::TILE_BYTES + (BF ? lane_base(trow, tchunk) : k_lane);
+    // chunk c (even) of block mb
+    auto chunk_addr = [](uint32_t base, int c, int mb) {
+      return (base ^ ((c & 7) << 4)) + (c >> 3) * C::BLOCK_BYTES + mb * 16 * C::ROWB;
     };
     uint32_t qf[NB][KS][2];
     float head_scale[NB][2];                     // multiplies the logits of heads 2t, 2t + 1
@@ -474,12 +482,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       ok = warp_wait(&sm.sync, meets++ & 1, &sm.abort, p.status);
       return ok;
     };
+    int tick = 0;
     for (int32_t i = 0; i < tiles && ok; ++i) {
       const int s = i % C::STAGES;
       if (!warp_wait(&sm.full[s], (i / C::STAGES) & 1, &sm.abort, p.status)) break;
       const DecodeTileHeader h = sm.hdr[s];
       const int32_t v0 = h.rows & 0xffff, v1 = h.rows >> 16;
-      const uint32_t kbase = ptx::smem_addr(ring + s * C::STAGE_BYTES), vbase = kbase + C::TILE_BYTES;
+      const uint32_t kbase = ptx::smem_addr(ring + s * C::STAGE_BYTES) + k_lane;
+      const uint32_t vbase = ptx::smem_addr(ring + s * C::STAGE_BYTES) + v_lane;
       const uint8_t* extra = extras + s * C::EXTRA_BYTES;
       if (h.flags & 1) {
         // ---- a chunk begins: query fragments, running values
@@ -525,8 +535,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           for (int mt = 0; mt < KS; ++mt) o[nb][mt][0] = o[nb][mt][1] = o[nb][mt][2] = o[nb][mt][3] = 0.f;
         }
       }
-      if (i % MB == turn && row0 + 16 * MB > v0 && row0 < v1) {
-        const bool edge = row0 < v0 || row0 + 16 * MB > v1;
+      const bool my_turn = C::TURNS == 1 || tick == turn;
+      tick = tick + 1 == C::TURNS ? 0 : tick + 1;
+      auto process = [&](auto edge_tile) {
+        constexpr bool edge = decltype(edge_tile)::value;  // some of the warp's tokens are hidden
         // ---- logits: rows = tokens g, g + 8 of each block; columns = heads 2t, 2t + 1
         float sc[MB][NB][4];
 #pragma unroll
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
               uint32_t a[4];
-              ldsm4(chunk_addr(kbase, lrow, 2 * ks + lchunk) + mb * 16 * C::ROWB, a);
+              ldsm4(chunk_addr(kbase, 2 * ks, mb), a);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
                 mma16816<true>(sc[mb][nb], a[0], a[1], a[2], a[3], qf[nb][ks][0], qf[nb][ks][1]);
@@ -550,11 +562,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
               uint32_t a[4];
-              ldsm4(chunk_addr(kbase, lrow, ks + lchunk) + mb * 16 * C::ROWB, a);
+              ldsm4(chunk_addr(kbase, ks, mb), a);
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t a0 = codes2<FMT>(a[2 * j]), a2 = codes2<FMT>(a[2 * j] >> 16);
-                const uint32_t a1 = codes2<FMT>(a[2 * j + 1]), a3 = codes2<FMT>(a[2 * j + 1] >> 16);
+                uint32_t a0, a1, a2, a3;
+                codes_to_half2x2<FMT, false>(a[2 * j], a0, a2);
+                codes_to_half2x2<FMT, false>(a[2 * j + 1], a1, a3);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
                   mma16816<false>(sc[mb][nb], a0, a1, a2, a3, qf[nb][ks + j][0], qf[nb][ks + j][1]);
@@ -567,8 +580,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
           const int r = row0 + 16 * mb + g;
-          in[mb][0] = r >= v0 && r < v1;
-          in[mb][1] = r + 8 >= v0 && r + 8 < v1;
+          in[mb][0] = !edge || (r >= v0 && r < v1);
+          in[mb][1] = !edge || (r + 8 >= v0 && r + 8 < v1);
           if (!BF) {
             const int page = 1 << p.log2_page;  // exponent bytes: [page of the tile][K, V][row]
             const uint8_t* y = extra + ((r >> p.log2_page) << p.log2_page) * 2 + (r & (page - 1));
@@ -592,7 +605,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
               const int32_t vy = __float_as_int(vscale[mb][j]);
               // a hidden token's byte may be anything: its weight is zero whatever that says
               vscale[mb][j] = vy == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(vy - vtop + 14);
-              if (!in[mb][j]) vscale[mb][j] = 0.f;
+              if (edge && !in[mb][j]) vscale[mb][j] = 0.f;
             }
         }
         uint32_t pf[MB][NB][2], pl[MB][NB][2];
@@ -662,7 +675,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; edge && j < 2; ++j) {
             const int r = row0 + 16 * mb + 8 * j + 2 * t;
             keep[mb][j] = (r >= v0 && r < v1 ? 0xffffu : 0u) | (r + 1 >= v0 && r + 1 < v1 ? 0xffff0000u : 0u);
           }
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
               uint32_t a[4];
-              ldsm4_t(chunk_addr(vbase, trow, 2 * mt + tchunk) + mb * 16 * C::ROWB, a);
+              ldsm4_t(chunk_addr(vbase, 2 * mt, mb), a);
               if (edge) {
                 a[0] &= keep[mb][0];
                 a[1] &= keep[mb][0];
@@ -691,12 +704,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
               uint32_t a[4];
-              ldsm4_t(chunk_addr(vbase, lrow, mt + lchunk) + mb * 16 * C::ROWB, a);
+              ldsm4_t(chunk_addr(vbase, mt, mb), a);
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 // bytes of a register: token 2t's codes of dims 2g, 2g+1, then token 2t+1's
-                const uint32_t x = __byte_perm(a[2 * j], 0, 0x3120), y = __byte_perm(a[2 * j + 1], 0, 0x3120);
-                uint32_t a0 = codes2<FMT>(x), a1 = codes2<FMT>(x >> 16), a2 = codes2<FMT>(y), a3 = codes2<FMT>(y >> 16);
+                uint32_t a0, a1, a2, a3;
+                codes_to_half2x2<FMT, true>(a[2 * j], a0, a1);
+                codes_to_half2x2<FMT, true>(a[2 * j + 1], a2, a3);
                 if (edge) {
                   a0 &= keep[mb][0];
                   a1 &= keep[mb][0];
@@ -709,6 +723,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
               }
             }
         }
+      };
+      if (my_turn && row0 + 16 * MB > v0 && row0 < v1) {
+        if (row0 < v0 || row0 + 16 * MB > v1) process(Flag<true>{});
+        else process(Flag<false>{});
       }
       if (!(h.flags & 2)) {
         __syncwarp();
@@ -716,7 +734,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         continue;
       }
 
-      // ---- a chunk ends: the eight warps' results become one, through the stage of its last tile
+      // ---- a chunk ends: the warps' results become one, through the stage of its last tile
       const int32_t b = h.b, h0 = h.h0, slot = (h.flags >> 2) - 1;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -738,25 +756,42 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int head = nb * 8 + 2 * t + j;
-          float ms[kDecodeWarps];
+          float ms[C::WARPS];
           top[j] = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < kDecodeWarps; ++x) {
+          for (int x = 0; x < C::WARPS; ++x) {
             ms[x] = sm.m[x][head];
             top[j] = fmaxf(top[j], ms[x]);
           }
           sum[j] = 0.f;
 #pragma unroll
-          for (int x = 0; x < kDecodeWarps; ++x)
+          for (int x = 0; x < C::WARPS; ++x)
             sum[j] += (ms[x] == -INFINITY ? 0.f : ptx::ex2(ms[x] - top[j])) * sm.l[x][head];
           w[j] = m[nb][j] == -INFINITY ? 0.f : ptx::ex2(m[nb][j] - top[j]);
           if (!BF) w[j] *= exp2_int(vref - 127 - 14);
         }
-        if (live)
+        float* mine_o = scratch + (warp & 7) * KS * 128 + lane;
+        float scaled[KS][4];
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) scaled[mt][c] = o[nb][mt][c] * w[c & 1];
+        auto put = [&] {
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) scratch[((warp * KS + mt) * 4 + c) * 32 + lane] = o[nb][mt][c] * w[c & 1];
+            for (int c = 0; c < 4; ++c) mine_o[(mt * 4 + c) * 32] = scaled[mt][c];
+        };
+        if (C::WARPS > 8) {  // the scratch has room for eight: the others' go to their partners first
+          if (warp >= 8 && live) put();
+          if (!meet()) break;
+          if (warp < C::WARPS - 8 && live)
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) scaled[mt][c] += mine_o[(mt * 4 + c) * 32];
+        }
+        if (warp < 8 && live) put();
         if (!meet()) break;
         // warp x finishes the 16 dims of m-tile x; this lane's heads are again 2t, 2t + 1
         if (warp < KS && live) {
@@ -764,9 +799,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float* from = scratch + (warp * 4 + c) * 32 + lane;
-            float part[kDecodeWarps];
+            float part[8];
 #pragma unroll
-            for (int x = 0; x < kDecodeWarps; ++x) part[x] = from[x * KS * 128];
+            for (int x = 0; x < 8; ++x) part[x] = from[x * KS * 128];
             v[c] = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
           }
           const int d0 = 16 * warp + (BF ? g : 2 * g), d1 = d0 + (BF ? 8 : 1);

@@ -230,10 +230,15 @@ template <int FMT>
 __device__ __forceinline__ void dequant16(uint4 w, float scale, uint32_t (&o)[8]) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(codes_to_half2<FMT>((i & 1) ? in[i / 2] >> 16 : in[i / 2]));
-    const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * scale, f.y * scale);
-    o[i] = *reinterpret_cast<const uint32_t*>(&r);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[2];
+    codes_to_half2x2<FMT, false>(in[i], h[0], h[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+      const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+      o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&r);
+    }
   }
 }
 

@@ -39,7 +39,7 @@ __device__ __forceinline__ float row_inverse_scale(int32_t y) { return __uint_as
 
 // 2^(y - 127), with 2^-127 (a subnormal) for y = 0 and NaN for y = 255.
 __device__ __forceinline__ float row_scale(int32_t y) {
-  const uint32_t bits = y == 0 ? 0x00400000u : (uint32_t)y << 23;
+  const uint32_t bits = max((uint32_t)y << 23, 0x00400000u);
   return __uint_as_float(y == kRowNaN ? 0x7fffffffu : bits);
 }
 
@@ -60,17 +60,29 @@ __device__ __forceinline__ uint32_t quantise4(uint32_t w0, uint32_t w1, float in
   return lo | (hi << 16);
 }
 
-// The two codes in the low 16 bits of w as fp16: both kinds of code are exact in fp16.
-template <int FMT>
-__device__ __forceinline__ __half2 codes_to_half2(uint32_t w) {
+// The four codes in w as two pairs of fp16 (both kinds of code are exact in fp16): a = bytes (0, 1) and b = bytes (2, 3),
+// or with CROSS a = bytes (0, 2) and b = bytes (1, 3).
+template <int FMT, bool CROSS>
+__device__ __forceinline__ void codes_to_half2x2(uint32_t w, uint32_t& a, uint32_t& b) {
   if (FMT == kFmtE4m3) {
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffff), __NV_E4M3);
-    return __half2(r);
+    if (CROSS) w = __byte_perm(w, 0, 0x3120);
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+  } else {
+    // 0x6400 | u is 1024 + u in fp16; with u = code + 128, taking 1152 off leaves the code, exactly
+    w ^= 0x80808080u;
+    a = __byte_perm(w, 0x64646464u, CROSS ? 0x4240 : 0x4140);
+    b = __byte_perm(w, 0x64646464u, CROSS ? 0x4341 : 0x4342);
+    const uint32_t off = 0x64806480u;
+    const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&off));
+    const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&off));
+    a = *reinterpret_cast<const uint32_t*>(&ha);
+    b = *reinterpret_cast<const uint32_t*>(&hb);
   }
-  // 0x6400 | u is 1024 + u in fp16; with u = code + 128, taking 1152 off leaves the code, exactly
-  const uint32_t biased = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
-  const uint32_t off = 0x64806480u;
-  return __hsub2(*reinterpret_cast<const __half2*>(&biased), *reinterpret_cast<const __half2*>(&off));
 }
 
 }  // namespace segpaged
