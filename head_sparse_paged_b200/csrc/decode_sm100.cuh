@@ -276,6 +276,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         sm.pair0 = u;
         sm.tile0 = (int32_t)min((long long)n, (lo_unit - at + 1) / 2);
         sm.first_rank = rank + sm.tile0;
+        if (per == 1 && sm.tile0 < n) {  // the run's first page ids will be wanted in a moment
+          const int32_t tile = sm.tile0;
+          const int64_t tok = tile < own.g.n_a ? (int64_t)tile * kDecodeTile
+                                               : own.g.b0 + (int64_t)(tile - own.g.n_a) * kDecodeTile;
+          const int32_t page = (int32_t)(tok >> p.log2_page);
+          const int64_t e = (int64_t)own.off + (page < own.n_sink ? page : page - own.w0 + own.n_sink);
+          if (e >= 0 && e < p.table_len) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + e));
+        }
       }
       if (hi_unit > at && hi_unit <= next) sm.end_rank = rank + min((long long)n, (hi_unit - at + 1) / 2);
       rank += n;
@@ -479,7 +487,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     auto meet = [&]() {                          // all consumer warps (bounded, unlike a block barrier)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.sync);
-      ok = warp_wait(&sm.sync, meets++ & 1, &sm.abort, p.status);
+      const uint32_t parity = meets++ & 1;
+      for (int spin = 0; spin < 256; ++spin)
+        if (__all_sync(0xffffffffu, ptx::mbar_test_wait(&sm.sync, parity))) return true;
+      ok = warp_wait(&sm.sync, parity, &sm.abort, p.status);
       return ok;
     };
     int tick = 0;
@@ -748,76 +759,98 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           }
         }
       if (!meet()) break;  // from here no warp reads the tile any more
-      float* scratch = reinterpret_cast<float*>(ring + s * C::STAGE_BYTES);  // [warp][KS * 4][lane]
+      float4* scratch = reinterpret_cast<float4*>(ring + s * C::STAGE_BYTES);  // [8][KS][lane]
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const bool live = nb * 8 + 2 * t < heads;  // this lane's columns are heads of the group
-        float top[2], sum[2], w[2];
+        // the largest m of this lane's two heads and the sum of all l to it: lane (g, t) looks at warps g and g + 8
+        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, w[2];
+        float2 mx[2], lx[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mx[x] = make_float2(-INFINITY, -INFINITY);
+          lx[x] = make_float2(0.f, 0.f);
+          if (8 * x + g < C::WARPS) {
+            mx[x] = *reinterpret_cast<const float2*>(&sm.m[8 * x + g][nb * 8 + 2 * t]);
+            lx[x] = *reinterpret_cast<const float2*>(&sm.l[8 * x + g][nb * 8 + 2 * t]);
+          }
+          top[0] = fmaxf(top[0], mx[x].x);
+          top[1] = fmaxf(top[1], mx[x].y);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], d));
+          top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], d));
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          sum[0] += (mx[x].x == -INFINITY ? 0.f : ptx::ex2(mx[x].x - top[0])) * lx[x].x;
+          sum[1] += (mx[x].y == -INFINITY ? 0.f : ptx::ex2(mx[x].y - top[1])) * lx[x].y;
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
+          sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], d);
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int head = nb * 8 + 2 * t + j;
-          float ms[C::WARPS];
-          top[j] = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < C::WARPS; ++x) {
-            ms[x] = sm.m[x][head];
-            top[j] = fmaxf(top[j], ms[x]);
-          }
-          sum[j] = 0.f;
-#pragma unroll
-          for (int x = 0; x < C::WARPS; ++x)
-            sum[j] += (ms[x] == -INFINITY ? 0.f : ptx::ex2(ms[x] - top[j])) * sm.l[x][head];
           w[j] = m[nb][j] == -INFINITY ? 0.f : ptx::ex2(m[nb][j] - top[j]);
           if (!BF) w[j] *= exp2_int(vref - 127 - 14);
         }
-        float* mine_o = scratch + (warp & 7) * KS * 128 + lane;
-        float scaled[KS][4];
+        float4* mine_o = scratch + (warp & 7) * KS * 32 + lane;
+        float4 scaled[KS];
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) scaled[mt][c] = o[nb][mt][c] * w[c & 1];
-        auto put = [&] {
-#pragma unroll
-          for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) mine_o[(mt * 4 + c) * 32] = scaled[mt][c];
-        };
+          scaled[mt] = make_float4(o[nb][mt][0] * w[0], o[nb][mt][1] * w[1], o[nb][mt][2] * w[0], o[nb][mt][3] * w[1]);
         if (C::WARPS > 8) {  // the scratch has room for eight: the others' go to their partners first
-          if (warp >= 8 && live) put();
+          if (warp >= 8 && live)
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) mine_o[mt * 32] = scaled[mt];
           if (!meet()) break;
           if (warp < C::WARPS - 8 && live)
 #pragma unroll
-            for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) scaled[mt][c] += mine_o[(mt * 4 + c) * 32];
+            for (int mt = 0; mt < KS; ++mt) {
+              const float4 v = mine_o[mt * 32];
+              scaled[mt].x += v.x;
+              scaled[mt].y += v.y;
+              scaled[mt].z += v.z;
+              scaled[mt].w += v.w;
+            }
         }
-        if (warp < 8 && live) put();
+        if (warp < 8 && live)
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) mine_o[mt * 32] = scaled[mt];
         if (!meet()) break;
         // warp x finishes the 16 dims of m-tile x; this lane's heads are again 2t, 2t + 1
         if (warp < KS && live) {
-          float v[4];
+          const float4* from = scratch + warp * 32 + lane;
+          float4 v[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float* from = scratch + (warp * 4 + c) * 32 + lane;
-            float part[8];
+          for (int x = 0; x < 8; ++x) v[x] = from[x * KS * 32];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) part[x] = from[x * KS * 128];
-            v[c] = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
-          }
+          for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+            for (int x = 0; x < d; ++x) {
+              v[x].x += v[x + d].x;
+              v[x].y += v[x + d].y;
+              v[x].z += v[x + d].z;
+              v[x].w += v[x + d].w;
+            }
+          const float out[2][2] = {{v[0].x, v[0].z}, {v[0].y, v[0].w}};  // [head][dim]
           const int d0 = 16 * warp + (BF ? g : 2 * g), d1 = d0 + (BF ? 8 : 1);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int head = nb * 8 + 2 * t + j;
             if (head >= heads) continue;
-            const float inv = 1.f / sum[j];
+            const float inv = __fdividef(1.f, sum[j]);
             if (slot < 0) {
-              __nv_bfloat16* out = p.o + ((int64_t)b * Hq + h0 + head) * D;
-              out[d0] = __float2bfloat16_rn(v[j] * inv);
-              out[d1] = __float2bfloat16_rn(v[2 + j] * inv);
+              __nv_bfloat16* to = p.o + ((int64_t)b * Hq + h0 + head) * D;
+              to[d0] = __float2bfloat16_rn(out[j][0] * inv);
+              to[d1] = __float2bfloat16_rn(out[j][1] * inv);
             } else {
-              float* out = p.part_o + ((int64_t)slot * kDecodeGroup + head) * D;
-              out[d0] = v[j] * inv;
-              out[d1] = v[2 + j] * inv;
+              float* to = p.part_o + ((int64_t)slot * kDecodeGroup + head) * D;
+              to[d0] = out[j][0] * inv;
+              to[d1] = out[j][1] * inv;
             }
             if (warp == 0 && g == 0) {
               const float lse2 = top[j] + log2f(sum[j]);
