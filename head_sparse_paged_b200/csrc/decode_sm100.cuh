@@ -39,8 +39,10 @@ namespace segpaged {
 
 constexpr int kDecodeTile = 128;         // tokens of a tile
 constexpr int kDecodeMaxWarps = 12;      // most consumer warps
+constexpr int kDecodeMaxProducers = 2;   // producer warps
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
+constexpr float kDecodeMinScale = 0x1p-120f;  // in place of a logit scale of 0: 0 x -infinity is not wanted
 constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
 
 struct DecodeParams {
@@ -71,7 +73,6 @@ struct DecodeCfg {
   static constexpr int WARPS = NB == 1 && FMT != kFmtBf16 ? 12 : 8;               // consumer warps
   static constexpr int TILE_WARPS = kDecodeTile / (16 * MB);     // of which these share a tile
   static constexpr int TURNS = WARPS / TILE_WARPS;
-  static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int EB = FMT == kFmtBf16 ? 2 : 1;             // bytes of an element
   static constexpr int ROWB = D * EB < 128 ? D * EB : 128;       // bytes of a row in one column block
   static constexpr int CB = D * EB / ROWB;                       // column blocks
@@ -85,11 +86,18 @@ struct DecodeCfg {
   static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
-  static_assert(STAGES >= 2, "ring");
+  // A producer's wait for a stage looks at one parity bit, so the stage may be at most one use behind it: what it waited
+  // for before its last tile, PRODUCERS tiles ago, has to cover the use before the last one, 2 STAGES tiles ago.
+  static constexpr int PRODUCERS = STAGES < kDecodeMaxProducers ? STAGES : kDecodeMaxProducers;
+  static constexpr int THREADS = 32 * (WARPS + PRODUCERS);
+  static_assert(STAGES >= 2 && STAGES <= 8 && PRODUCERS <= STAGES, "ring");
   static_assert(STAGE_BYTES >= 8 * 8 * D * 4, "a stage holds eight warps' O of one column block");
-  // What ending a chunk costs a CTA, in half tiles (about 1 us, against 1.6 us for a bf16 tile and 0.8 us for an 8-bit
-  // one of 128 columns).
-  static constexpr int PAIR_COST = FMT == kFmtBf16 ? 1 : 2;
+  // What ending a pair costs a CTA, in half tiles.
+#ifndef PC8
+#define PC8 5
+#define PC16 2
+#endif
+  static constexpr int PAIR_COST = (FMT == kFmtBf16 ? PC16 : PC8) * 128 / D;
 };
 
 template <bool B>
@@ -189,13 +197,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, status, kDecodeStatusTimeout));
 }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)),
+               "l"((uint64_t)__cvta_generic_to_global(src))
+               : "memory");
+}
+// Arrives on `bar` (one of its expected arrivals) when this thread's earlier cp.async copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
+}
+
 // Shared memory beside the ring (4096 bytes).
 struct DecodeSmall {
   uint64_t full[8], empty[8];
   uint64_t sync;                                // consumers' meeting point
   DecodeTileHeader hdr[8];
   float m[kDecodeMaxWarps][16], l[kDecodeMaxWarps][16];
-  long long warp_sum[kDecodeMaxWarps + 1];
+  long long warp_sum[kDecodeMaxWarps + kDecodeMaxProducers];
   long long first_rank, end_rank;               // this CTA's run in the list of all tiles
   int32_t pair0, tile0;                         // where its first tile lies
   int32_t abort;
@@ -218,7 +236,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(&sm.full[s], 1);
+      ptx::mbar_init(&sm.full[s], BF ? 1 : 33);  // the copies' bytes; for 8-bit pools also each lane's cp.async
       ptx::mbar_init(&sm.empty[s], C::WARPS);
     }
     ptx::mbar_init(&sm.sync, C::WARPS);
@@ -255,7 +273,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w <= C::WARPS; ++w) {
+  for (int w = 0; w < C::WARPS + C::PRODUCERS; ++w) {
     const long long x = sm.warp_sum[w];
     if (w < warp) before += x;
     total += x;
@@ -312,9 +330,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     __syncthreads();
   }
 
-  if (warp == C::WARPS) {
+  if (warp >= C::WARPS) {
     // ------------------------------------------------------------------------------------ producer
-    // Works in batches of 32 boxes (a box: up to 64 rows of one page; 2 to 8 to a tile), one per lane: the lanes find
+    // Producer j does tiles j, j + kStep, ... of the run: preparing and issuing a tile's copies takes a warp 0.5 us (pages of
+    // 64 rows) to 0.9 us (of 16), as long as the bytes take, and is a chain of latencies that several warps overlap.
+    // Each works in batches of 32 boxes (a box: up to 64 rows of one page; 2 to 8 to a tile), one per lane: the lanes find
     // their boxes' pages for the next batch, whose loads are then in flight while this batch's copies are issued.
     // (Looking one tile ahead instead left 0.9 us per tile, the latency of a page id under load: 5.0 TB/s of an
     // all-global layer's 2.2 GB.)
@@ -322,6 +342,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     const int32_t log2_box = min(p.log2_page, 6), box = 1 << log2_box;  // rows of one TMA box
     const int32_t boxes = kDecodeTile >> log2_box, batch_tiles = 32 / boxes;
     const int32_t my_tile = lane / boxes, my_row = (lane % boxes) * box;
+    constexpr int32_t kStep = C::PRODUCERS;
     // Window: lane k holds pair window + k, whose tiles are [w_end - w.g.n, w_end) of this CTA's run.
     int32_t window = 0, w_end = 0;
     DecodePair w = {};
@@ -342,7 +363,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       bool need;        // a visible token lies in it
       DecodeTileHeader h;
     } cur, nxt;
-    // The boxes of tiles i0, i0 + 1, ... into nxt; returns how many tiles that are (0: the run is done).
+    // The boxes of tiles i0, i0 + kStep, ... into nxt; returns how many tiles that are (0: the run is done).
     auto plan = [&](int32_t i0) -> int32_t {
       nxt.need = false;
       if (i0 >= tiles) return 0;
@@ -356,7 +377,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         stop = __shfl_sync(0xffffffffu, w_end, 31);
       }
       stop = min(stop, tiles);
-      const int32_t i = min(i0 + my_tile, stop - 1);
+      const int32_t i = min(i0 + my_tile * kStep, stop - 1);
       int32_t k = 0;  // pairs of the window that end at or before tile i
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1)
@@ -377,7 +398,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       nxt.h.b = __shfl_sync(0xffffffffu, w.b, k);
       nxt.h.h0 = __shfl_sync(0xffffffffu, w.h0, k);
       nxt.h.flags = (tile == 0 || i == 0 ? 1 : 0) | (last ? 2 : 0);
-      const bool mine = i0 + my_tile < stop;
+      const bool mine = i0 + my_tile * kStep < stop;
       if (last) {
         const bool from_start = tile <= i, to_end = tile + 1 == n;  // does the chunk hold the pair's first, last tile
         if (!(from_start && to_end)) nxt.h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
@@ -399,21 +420,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         if (t >= len || off < 0 || (int64_t)off + t >= p.table_len) report(p.status, 2);
         else nxt.id = __ldg(p.table + off + t);  // nothing waits for it before its batch is issued
       }
-      return min(batch_tiles, stop - i0);
+      return min(batch_tiles, (stop - i0 + kStep - 1) / kStep);
     };
     if (tiles > 0) {
       load_window(sm.pair0, -sm.tile0, per == 1);
-      int32_t i = 0, count = plan(0);
-      uint32_t issued = 0;
+      int32_t i = warp - C::WARPS, count = plan(i), issued = -1;  // issued: the last tile
       bool ok = true;
       while (count > 0 && ok) {
         cur = nxt;
-        const int32_t next_count = plan(i + count);
+        const int32_t next_count = plan(i + count * kStep);
         if (cur.need && (uint32_t)cur.id >= (uint32_t)p.num_pages) {
           report(p.status, 1);
           cur.id = 0;
         }
-        for (int32_t j = 0; j < count; ++j, ++i) {
+        for (int32_t j = 0; j < count; ++j, i += kStep) {
           const int s = i % C::STAGES;
           uint8_t* stage = ring + s * C::STAGE_BYTES;
           uint8_t* extra = extras + s * C::EXTRA_BYTES;
@@ -423,20 +443,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           }
           const bool load = my_tile == j && cur.need;
           const uint32_t have = __ballot_sync(0xffffffffu, load);
-          // one copy of a page's exponent bytes: by the first of its boxes that is loaded
-          const uint32_t before_it = p.log2_page == log2_box ? 0u : ((1u << (lane & 1)) - 1u) << (lane & 30);
-          const bool scales = !BF && load && (have & before_it) == 0;
-          const uint32_t n_scales = BF ? 0 : __popc(__ballot_sync(0xffffffffu, scales));
           if (lane == j * boxes) {
             const bool with_q = cur.h.flags & 1;
             sm.hdr[s] = cur.h;
-            ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + n_scales * 2 * page +
-                                                        (with_q ? heads * D * 2 : 0));
+            ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + (with_q ? heads * D * 2 : 0));
             if (with_q) {
               bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)cur.h.b * Hq + cur.h.h0) * D, heads * D * 2, &sm.full[s]);
             }
           }
-          issued = i + 1;
+          issued = i;
           __syncwarp();
           if (load) {
 #pragma unroll
@@ -445,9 +460,17 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
               ptx::tma_load_3d(stage + at, &tk, cb * (C::ROWB / C::EB), cur.row, cur.id, &sm.full[s]);
               ptx::tma_load_3d(stage + C::TILE_BYTES + at, &tv, cb * (C::ROWB / C::EB), cur.row, cur.id, &sm.full[s]);
             }
-            if (scales)
-              bulk_load(extra + ((my_row >> p.log2_page) << p.log2_page) * 2, p.kv_scale + (int64_t)cur.id * 2 * page,
-                        2 * page, &sm.full[s]);
+          }
+          if (!BF) {
+            // The tile's exponent bytes, [page][K, V][row], 16 of them a lane: a bulk copy per page would be as many
+            // copies again as the codes take where pages are small.
+            const int32_t at = lane * 16, from = j * boxes + ((at >> (p.log2_page + 1)) << p.log2_page >> log2_box);
+            // of a page of two boxes, either may be the only one that is loaded
+            const int32_t box_at = (p.log2_page == log2_box || (have >> (from & 31) & 1) ? from : from + 1) & 31;
+            const int32_t id = __shfl_sync(0xffffffffu, cur.id, box_at);
+            if (lane < C::SCALE_BYTES / 16 && (have >> box_at & 1))
+              cp_async16(extra + at, p.kv_scale + ((int64_t)id << (p.log2_page + 1)) + (at & (2 * page - 1)));
+            cp_async_arrive(&sm.full[s]);
           }
           __syncwarp();
         }
@@ -455,8 +478,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       }
       // after a timeout: the copies in flight land before the block's memory is given up
       if (sm.abort)
-        for (uint32_t i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
-          ptx::mbar_wait(&sm.full[i % C::STAGES], (i / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
+        for (int32_t k = issued; k >= 0 && k > issued - C::STAGES; k -= kStep)
+          ptx::mbar_wait(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
     }
   } else {
     // ----------------------------------------------------------------------------------- consumers
@@ -479,7 +502,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       return (base ^ ((c & 7) << 4)) + (c >> 3) * C::BLOCK_BYTES + mb * 16 * C::ROWB;
     };
     uint32_t qf[NB][KS][2];
-    float head_scale[NB][2];                     // multiplies the logits of heads 2t, 2t + 1
+    // Logits are kept as y = (+-q') . k' with the K row's exponent in, which f = head_scale > 0 takes to log2 units: the
+    // maximum m is one of y, and a probability 2^(f y - f m) is one fma and one ex2.
+    float head_scale[NB][2];                     // of heads 2t, 2t + 1
     float m[NB][2], l[NB][2], o[NB][KS][4];
     int32_t vref = 0;                            // r + 127
     uint32_t meets = 0;
@@ -493,10 +518,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       ok = warp_wait(&sm.sync, parity, &sm.abort, p.status);
       return ok;
     };
-    int tick = 0;
+    int tick = 0, s = -1;
+    uint32_t phase = 1;
     for (int32_t i = 0; i < tiles && ok; ++i) {
-      const int s = i % C::STAGES;
-      if (!warp_wait(&sm.full[s], (i / C::STAGES) & 1, &sm.abort, p.status)) break;
+      s = s + 1 == C::STAGES ? 0 : s + 1;
+      phase ^= s == 0;
+      if (!warp_wait(&sm.full[s], phase, &sm.abort, p.status)) break;
       const DecodeTileHeader h = sm.hdr[s];
       const int32_t v0 = h.rows & 0xffff, v1 = h.rows >> 16;
       const uint32_t kbase = ptx::smem_addr(ring + s * C::STAGE_BYTES) + k_lane;
@@ -517,11 +544,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
               // fp16: the contraction runs in the order the code bytes lie in, 4t .. 4t+3 of each 16
               const int d = 16 * ks + (BF ? 2 * t + 8 * j : 4 * t + 2 * j);
               qf[nb][ks][j] = head < heads ? *reinterpret_cast<const uint32_t*>(qs + head * D + d) : 0u;
+              if (p.scale_log2 < 0.f) qf[nb][ks][j] ^= 0x80008000u;
               top = absmax2(top, qf[nb][ks][j]);
             }
           }
           if (BF) {
-            head_scale[nb][0] = head_scale[nb][1] = p.scale_log2;
+            head_scale[nb][0] = head_scale[nb][1] = fmaxf(fabsf(p.scale_log2), kDecodeMinScale);
           } else {
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -533,7 +561,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 qf[nb][ks][j] = pack_f16x2(bf16_lo(qf[nb][ks][j]) * up, bf16_hi(qf[nb][ks][j]) * up);
-            const float back = p.scale_log2 * exp2_int(-e);
+            const float back = fmaxf(fabsf(p.scale_log2) * exp2_int(-e), kDecodeMinScale);
             head_scale[nb][0] = __shfl_sync(0xffffffffu, back, 8 * t);
             head_scale[nb][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
           }
@@ -586,37 +614,31 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             }
         }
         bool in[MB][2];
-        float kscale[MB][2], vscale[MB][2], vshift = 1.f;
-        int32_t vtop = 0;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
           const int r = row0 + 16 * mb + g;
           in[mb][0] = !edge || (r >= v0 && r < v1);
           in[mb][1] = !edge || (r + 8 >= v0 && r + 8 < v1);
-          if (!BF) {
-            const int page = 1 << p.log2_page;  // exponent bytes: [page of the tile][K, V][row]
-            const uint8_t* y = extra + ((r >> p.log2_page) << p.log2_page) * 2 + (r & (page - 1));
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              kscale[mb][j] = row_scale(y[8 * j]);
-              const int32_t vy = y[page + 8 * j];
-              vscale[mb][j] = __int_as_float(vy);  // the byte, until the largest one is known
-              if (in[mb][j] && vy != kRowNaN) vtop = max(vtop, vy);
-            }
-          }
         }
+        // Exponents: lane x works out token x's (of the warp's 16 MB), the lanes that hold its logits fetch them.
+        float kscale[MB][2], vscale[MB][2], vshift = 1.f;
         if (!BF) {
-          vtop = max(vref, __reduce_max_sync(0xffffffffu, vtop));
-          vshift = exp2_int(vref - vtop);
-          vref = vtop;
+          const int r = row0 + (lane & (16 * MB - 1));
+          const uint8_t* at = extra + r + (r >> p.log2_page << p.log2_page);  // [page of the tile][K, V][row]
+          const float k_mine = row_scale(at[0]);
+          const int32_t y = at[1 << p.log2_page];
+          const bool seen = !edge || (r >= v0 && r < v1);
+          const int32_t top = max(vref, __reduce_max_sync(0xffffffffu, seen && y != kRowNaN ? y : 0));
+          // a hidden token's byte may be anything: its weight is zero whatever that says
+          const float v_mine = !seen ? 0.f : y == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(y - top + 14);
+          vshift = exp2_int(vref - top);
+          vref = top;
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int32_t vy = __float_as_int(vscale[mb][j]);
-              // a hidden token's byte may be anything: its weight is zero whatever that says
-              vscale[mb][j] = vy == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(vy - vtop + 14);
-              if (edge && !in[mb][j]) vscale[mb][j] = 0.f;
+              kscale[mb][j] = __shfl_sync(0xffffffffu, k_mine, 16 * mb + 8 * j + g);
+              vscale[mb][j] = __shfl_sync(0xffffffffu, v_mine, 16 * mb + 8 * j + g);
             }
         }
         uint32_t pf[MB][NB][2], pl[MB][NB][2];
@@ -630,8 +652,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             for (int j = 0; j < 2; ++j) {
               float& x0 = sc[mb][nb][2 * j];
               float& x1 = sc[mb][nb][2 * j + 1];
-              x0 *= BF ? f0 : kscale[mb][j] * f0;
-              x1 *= BF ? f1 : kscale[mb][j] * f1;
+              if (!BF) {
+                x0 *= kscale[mb][j];
+                x1 *= kscale[mb][j];
+              }
               if (edge) {
                 x0 = in[mb][j] ? x0 : -INFINITY;
                 x1 = in[mb][j] ? x1 : -INFINITY;
@@ -648,8 +672,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           n1 = fmaxf(n1, m[nb][1]);
           // a larger maximum (or V exponent) rescales what was summed so far
           if (__any_sync(0xffffffffu, n0 != m[nb][0] || n1 != m[nb][1] || vshift != 1.f)) {
-            const float c0 = m[nb][0] == -INFINITY ? 0.f : ptx::ex2(m[nb][0] - n0);
-            const float c1 = m[nb][1] == -INFINITY ? 0.f : ptx::ex2(m[nb][1] - n1);
+            const float c0 = m[nb][0] == -INFINITY ? 0.f : ptx::ex2(f0 * (m[nb][0] - n0));
+            const float c1 = m[nb][1] == -INFINITY ? 0.f : ptx::ex2(f1 * (m[nb][1] - n1));
             // NaN sums stay NaN: 0 * NaN
             l[nb][0] *= c0;
             l[nb][1] *= c1;
@@ -664,12 +688,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             m[nb][0] = n0;
             m[nb][1] = n1;
           }
-          const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
+          const float b0 = n0 == -INFINITY ? 0.f : -f0 * n0, b1 = n1 == -INFINITY ? 0.f : -f1 * n1;
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float p0 = ptx::ex2(sc[mb][nb][2 * j] - b0), p1 = ptx::ex2(sc[mb][nb][2 * j + 1] - b1);
+              const float p0 = ptx::ex2(fmaf(sc[mb][nb][2 * j], f0, b0)), p1 = ptx::ex2(fmaf(sc[mb][nb][2 * j + 1], f1, b1));
               l[nb][0] += p0;
               l[nb][1] += p1;
               if (BF) {
@@ -753,6 +777,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
+          if (m[nb][j] != -INFINITY) m[nb][j] *= head_scale[nb][j];  // to log2 units
           if (g == 0) {
             sm.m[warp][nb * 8 + 2 * t + j] = m[nb][j];
             sm.l[warp][nb * 8 + 2 * t + j] = l[nb][j];
@@ -870,57 +895,56 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 }
 
 // Joins the chunks of the pairs that several CTAs shared: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
-// Block (c, head) does the pair whose first chunk CTA c left; its other chunks lie in the first slots of the CTAs
-// after it. The warps take every kCombineWarps-th chunk each, a lane D/32 columns, and are merged in order.
+// CTA c's last pair, if it goes on behind it, has n chunks: CTA c's second slot and the first slots of the n - 1 CTAs
+// after it. Block (c, head) joins them: each of its eight warps takes every eighth chunk, a lane D/32 columns, and the
+// warps' sums are added in order. The loads of four chunks a warp are in flight together with those of all the log
+// sums, so a pair of up to 32 chunks waits for memory twice (which pair, then its chunks), one of 148 five times.
 constexpr int kDecodeCombineWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kDecodeCombineWarps) decode_combine_kernel(const DecodeParams p) {
-  constexpr int E = D / 32, NW = kDecodeCombineWarps;
-  constexpr int U = kDecodeMaxCtas / NW / 2;  // chunks of a warp whose loads are issued together
+__global__ void __launch_bounds__(32 * kDecodeCombineWarps, 6) decode_combine_kernel(const DecodeParams p) {
+  constexpr int E = D / 32, NW = kDecodeCombineWarps, U = 4;
   __shared__ float s_lse[kDecodeMaxCtas], s_sum[NW], s_top[NW], s_o[NW][D];
   const int32_t cta = blockIdx.x, head = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results of the launch before this one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int32_t pair = p.part_meta[2 * cta], n = min(p.part_meta[2 * cta + 1], kDecodeMaxCtas);
+  const int2 meta = *reinterpret_cast<const int2*>(p.part_meta + 2 * cta);
+  const int32_t pair = meta.x, n = min(meta.y, kDecodeMaxCtas);
   if (n <= 1) return;
-  auto slot = [&](int32_t c) { return (int64_t)(c == 0 ? 2 * cta + 1 : 2 * (cta + c)) * kDecodeGroup + head; };
-  // log2 sums: their maximum, and the sum of the weights 2^(lse - maximum)
-  float top = -INFINITY;
-  for (int32_t c = threadIdx.x; c < n; c += 32 * NW) {
-    const float x = p.part_lse[slot(c)];
-    s_lse[c] = x;
-    top = fmaxf(top, x);
-  }
-  float o[E] = {};
+  auto slot = [&](int32_t c) { return (c == 0 ? 2 * cta + 1 : 2 * (cta + c)) * kDecodeGroup + head; };
   float v[U][E];
   auto load = [&](int32_t c0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int32_t c = c0 + u * NW;
       if (c >= n) continue;
-      const float* from = p.part_o + slot(c) * D + lane * E;
+      const float* from = p.part_o + (int64_t)slot(c) * D + lane * E;
       if (E == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(from);
       else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(from);
     }
   };
   load(warp);  // on its way while the weights are worked out
+  float top = -INFINITY;
+  for (int32_t c = threadIdx.x; c < n; c += 32 * NW) {
+    const float x = p.part_lse[slot(c)];
+    s_lse[c] = x;
+    top = fmaxf(top, x);
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (lane == 0) s_top[warp] = top;
   __syncthreads();
 #pragma unroll
   for (int x = 0; x < NW; ++x) top = fmaxf(top, s_top[x]);
-  auto weight = [&](int32_t c) { return s_lse[c] == -INFINITY ? 0.f : ptx::ex2(s_lse[c] - top); };
-  float sum = 0.f;
+  float sum = 0.f, o[E] = {};
   for (int32_t c0 = warp; c0 < n; c0 += U * NW) {
     if (c0 != warp) load(c0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int32_t c = c0 + u * NW;
       if (c >= n) continue;
-      const float w = weight(c);
+      const float w = s_lse[c] == -INFINITY ? 0.f : ptx::ex2(s_lse[c] - top);
       sum += w;
 #pragma unroll
       for (int k = 0; k < E; ++k) o[k] += w == 0.f ? 0.f : w * v[u][k];
@@ -941,7 +965,7 @@ __global__ void __launch_bounds__(32 * kDecodeCombineWarps) decode_combine_kerne
   }
   const int32_t bk = pair >> p.log2_hg, b = bk / p.Hkv;
   const int32_t h = (bk - b * p.Hkv) * p.G + (pair - (bk << p.log2_hg)) * kDecodeGroup + head;
-  p.o[((int64_t)b * p.Hkv * p.G + h) * D + d] = __float2bfloat16_rn(acc / sum);
+  p.o[((int64_t)b * p.Hkv * p.G + h) * D + d] = __float2bfloat16_rn(__fdividef(acc, sum));
   if (d == 0) p.lse[(int64_t)h * p.B + b] = 0.6931471805599453f * (top + log2f(sum));
 }
 
