@@ -146,7 +146,11 @@ __device__ __forceinline__ DecodePair decode_pair(const DecodeParams& p, int32_t
   r.n_sink = (int32_t)(((uint32_t)sink + last) >> lp);
   r.w0 = (int32_t)(max((int64_t)L - lq - win + 1, (int64_t)0) >> lp);
   if (global || r.w0 <= r.n_sink) r.n_sink = r.w0 = n_all;
-  if (r.g.n > 0 && r.len != r.n_sink + n_all - r.w0) report(p.status, 2);
+  // A table that does not hold exactly these pages: the pair is reported and left out.
+  if (L > 0 && (r.len != r.n_sink + n_all - r.w0 || r.off < 0 || r.off > p.table_len - r.len)) {
+    report(p.status, 2);
+    r.g.n = 0;
+  }
   return r;
 }
 
@@ -213,8 +217,8 @@ struct DecodeSmall {
   uint64_t sync;                                // consumers' meeting point
   DecodeTileHeader hdr[8];
   float m[kDecodeMaxWarps][16], l[kDecodeMaxWarps][16];
-  long long warp_sum[kDecodeMaxWarps + kDecodeMaxProducers];
-  long long first_rank, end_rank;               // this CTA's run in the list of all tiles
+  int32_t warp_sum[kDecodeMaxWarps + kDecodeMaxProducers];
+  int32_t first_rank, end_rank;                 // this CTA's run in the list of all tiles
   int32_t pair0, tile0;                         // where its first tile lies
   int32_t abort;
   DecodePair window[32];                        // pairs pair0 ..
@@ -256,61 +260,59 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   const int32_t per = (pairs + C::THREADS - 1) / C::THREADS;
   const int32_t u_lo = min((int32_t)threadIdx.x * per, pairs), u_hi = min(u_lo + per, pairs);
   DecodePair own = {};
-  long long mine = 0;
+  int32_t mine = 0;  // the tiles are fewer than the entries of the page table
   if (per == 1) {
     if (u_lo < u_hi) own = decode_pair(p, u_lo);
     mine = own.g.n;
   } else {
     for (int32_t u = u_lo; u < u_hi; ++u) mine += decode_pair(p, u).g.n;
   }
-  long long incl = mine;
+  int32_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+    const int32_t x = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += x;
   }
   if (lane == 31) sm.warp_sum[warp] = incl;
   __syncthreads();
-  long long before = incl - mine, total = 0;
+  int32_t before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < C::WARPS + C::PRODUCERS; ++w) {
-    const long long x = sm.warp_sum[w];
+    const int32_t x = sm.warp_sum[w];
     if (w < warp) before += x;
     total += x;
   }
-  const long long units = 2 * total + (long long)C::PAIR_COST * pairs;
+  const uint32_t units = 2u * total + (uint32_t)C::PAIR_COST * pairs;
   // every CTA that takes part has two units or more, so one in the middle of a pair has a tile of it
-  const int32_t ctas = (int32_t)min((long long)gridDim.x, max(units / 2, 1ll));
-  const long long share = units <= 0xffffffffll ? (long long)((uint32_t)units / (uint32_t)ctas) : units / ctas;
-  const int32_t spare = (int32_t)(units - share * ctas);  // the first `spare` CTAs take one unit more
-  const long long lo_unit = cta < ctas ? share * cta + min(cta, spare) : units;
-  const long long hi_unit = cta < ctas ? lo_unit + share + (cta < spare) : units;
-  {
-    long long rank = before;
+  const uint32_t ctas = min(gridDim.x, max(units / 2, 1u));
+  const uint32_t share = units / ctas, spare = units - share * ctas;  // the first `spare` CTAs take one unit more
+  const bool takes_part = cta < (int32_t)ctas;
+  const uint32_t lo_unit = share * cta + min((uint32_t)cta, spare), hi_unit = lo_unit + share + ((uint32_t)cta < spare);
+  if (takes_part) {
+    int32_t rank = before;
     for (int32_t u = u_lo; u < u_hi; ++u) {
       const int32_t n = per == 1 ? own.g.n : decode_pair(p, u).g.n;
-      const long long at = 2 * rank + (long long)C::PAIR_COST * u, next = at + 2 * n + C::PAIR_COST;
+      const uint32_t at = 2u * rank + (uint32_t)C::PAIR_COST * u, next = at + 2u * n + C::PAIR_COST;
       if (lo_unit >= at && lo_unit < next) {
+        const int32_t tile = min(n, (int32_t)(lo_unit - at + 1) / 2);
         sm.pair0 = u;
-        sm.tile0 = (int32_t)min((long long)n, (lo_unit - at + 1) / 2);
-        sm.first_rank = rank + sm.tile0;
-        if (per == 1 && sm.tile0 < n) {  // the run's first page ids will be wanted in a moment
-          const int32_t tile = sm.tile0;
+        sm.tile0 = tile;
+        sm.first_rank = rank + tile;
+        if (per == 1 && tile < n) {  // the run's first page ids will be wanted in a moment
           const int64_t tok = tile < own.g.n_a ? (int64_t)tile * kDecodeTile
                                                : own.g.b0 + (int64_t)(tile - own.g.n_a) * kDecodeTile;
           const int32_t page = (int32_t)(tok >> p.log2_page);
-          const int64_t e = (int64_t)own.off + (page < own.n_sink ? page : page - own.w0 + own.n_sink);
-          if (e >= 0 && e < p.table_len) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + e));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + own.off + (page < own.n_sink ? page : page - own.w0 + own.n_sink)));
         }
       }
-      if (hi_unit > at && hi_unit <= next) sm.end_rank = rank + min((long long)n, (hi_unit - at + 1) / 2);
+      if (hi_unit > at && hi_unit <= next) sm.end_rank = rank + min(n, (int32_t)(hi_unit - at + 1) / 2);
       rank += n;
     }
   }
   // pairs without a visible key (an empty sequence): O = 0, LSE = -inf, written by one CTA each
   const int32_t heads = min(p.G, kDecodeGroup), Hq = p.Hkv * p.G;
   for (int32_t u = u_lo; u < u_hi; ++u) {
-    if (per == 1 ? own.g.n > 0 : p.ctx_len[(u >> p.log2_hg) / p.Hkv] > 0) continue;
+    if (per == 1 ? own.g.L > 0 : p.ctx_len[(u >> p.log2_hg) / p.Hkv] > 0) continue;
     if (u % (int32_t)gridDim.x != cta) continue;
     const DecodePair e = decode_pair(p, u);
     uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)e.b * Hq + e.h0) * D);
@@ -322,8 +324,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     p.part_meta[2 * cta + 1] = 0;
   }
   __syncthreads();
-  const long long first_rank = sm.first_rank;
-  const int32_t tiles = cta < ctas ? (int32_t)max(sm.end_rank - first_rank, 0ll) : 0;
+  const int32_t first_rank = sm.first_rank, tiles = max(sm.end_rank - first_rank, 0);
   if (per == 1) {
     const int32_t k = (int32_t)threadIdx.x - sm.pair0;
     if (k >= 0 && k < 32) sm.window[k] = own;
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       const int32_t n_a = __shfl_sync(0xffffffffu, w.g.n_a, k), b0 = __shfl_sync(0xffffffffu, w.g.b0, k);
       const int32_t a1 = __shfl_sync(0xffffffffu, w.g.a1, k), lo_k = __shfl_sync(0xffffffffu, w.g.lo, k);
       const int32_t L = __shfl_sync(0xffffffffu, w.g.L, k), off = __shfl_sync(0xffffffffu, w.off, k);
-      const int32_t len = __shfl_sync(0xffffffffu, w.len, k), sink = __shfl_sync(0xffffffffu, w.n_sink, k);
+      const int32_t sink = __shfl_sync(0xffffffffu, w.n_sink, k);
       const int32_t w0 = __shfl_sync(0xffffffffu, w.w0, k);
       const int32_t tile = i - (end_k - n);
       const bool in_sink = tile < n_a;
@@ -404,9 +405,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         if (!(from_start && to_end)) nxt.h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
         if (mine && from_start && !to_end && my_row == 0) {
           // the pair goes on in the CTAs after this one, to the CTA that holds its last tile
-          const long long at = 2 * (first_rank + end_k - 1) + (long long)C::PAIR_COST * (window + k);  // its unit
-          const long long wide = (share + 1) * spare;  // units of the CTAs that take one more
-          const int32_t to = at < wide ? (int32_t)(at / (share + 1)) : spare + (int32_t)((at - wide) / share);
+          const uint32_t at = 2u * (first_rank + end_k - 1) + (uint32_t)C::PAIR_COST * (window + k);  // its unit
+          const uint32_t wide = (share + 1) * spare;  // units of the CTAs that take one more
+          const int32_t to = at < wide ? at / (share + 1) : spare + (at - wide) / share;
           p.part_meta[2 * cta] = window + k;
           p.part_meta[2 * cta + 1] = to - cta + 1;
         }
@@ -415,10 +416,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       nxt.need = mine && my_tile < batch_tiles && tok + box > lo && tok < hi;
       nxt.row = (int32_t)(tok & (page - 1));
       nxt.id = 0;
-      if (nxt.need) {
-        const int32_t lp = (int32_t)(tok >> p.log2_page), t = lp < sink ? lp : lp - w0 + sink;
-        if (t >= len || off < 0 || (int64_t)off + t >= p.table_len) report(p.status, 2);
-        else nxt.id = __ldg(p.table + off + t);  // nothing waits for it before its batch is issued
+      if (nxt.need) {  // nothing waits for the load before its batch is issued
+        const int32_t lp = (int32_t)(tok >> p.log2_page);
+        nxt.id = __ldg(p.table + off + (lp < sink ? lp : lp - w0 + sink));
       }
       return min(batch_tiles, (stop - i0 + kStep - 1) / kStep);
     };
