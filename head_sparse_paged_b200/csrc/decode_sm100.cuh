@@ -92,12 +92,9 @@ struct DecodeCfg {
   static constexpr int THREADS = 32 * (WARPS + PRODUCERS);
   static_assert(STAGES >= 2 && STAGES <= 8 && PRODUCERS <= STAGES, "ring");
   static_assert(STAGE_BYTES >= 8 * 8 * D * 4, "a stage holds eight warps' O of one column block");
-  // What ending a pair costs a CTA, in half tiles.
-#ifndef PC8
-#define PC8 5
-#define PC16 2
-#endif
-  static constexpr int PAIR_COST = (FMT == kFmtBf16 ? PC16 : PC8) * 128 / D;
+  // What ending a pair costs a CTA, in half tiles: about 2.5 us. Of 5, 7, 9 and 12 for 8-bit pools of 128 columns 9
+  // measured best on 32 sequences of 16-32K (66.8, 65.6, 65.0, 66.5 us), 2, 3 and 4 for bf16 alike (106.1 to 105.8).
+  static constexpr int PAIR_COST = (FMT == kFmtBf16 ? 4 : 8) * 128 / D;
 };
 
 template <bool B>
@@ -123,31 +120,27 @@ struct DecodePair {
   int32_t off, len, n_sink, w0, b, h0;
 };
 
-// Pair u: (sequence, KV head, pass of 16 query heads), u = (b * Hkv + k) << log2_hg | pass. The page rule is
-// storage_split's, with shifts for its divisions: this runs at the start of every launch, before the first load.
+// Pair u: (sequence, KV head, pass of 16 query heads), u = (b * Hkv + k) << log2_hg | pass.
 __device__ __forceinline__ DecodePair decode_pair(const DecodeParams& p, int32_t u) {
   const int32_t bk = u >> p.log2_hg;
   DecodePair r;
   r.b = bk / p.Hkv;
   r.h0 = (bk - r.b * p.Hkv) * p.G + (u - (bk << p.log2_hg)) * kDecodeGroup;
-  const int32_t L = max(p.ctx_len[r.b], 0), lq = max(p.q_len ? p.q_len[r.b] : 1, 1);
-  const int32_t global = p.cls[3 * bk], sink = min(max(p.cls[3 * bk + 1], 0), L), win = max(p.cls[3 * bk + 2], 1);
+  const HeadPages hp = head_pages(p.ctx_len, p.q_len, p.cls, r.b, bk, p.log2_page, 1);
+  const int32_t L = hp.L, lp = p.log2_page;
   r.off = p.offs[bk];
   r.len = p.offs[bk + 1] - r.off;
-  const int32_t lp = p.log2_page, last = (1 << lp) - 1;
+  r.n_sink = hp.n_sink;
+  r.w0 = hp.w0;
   r.g.L = L;
-  r.g.lo = max(L - win, 0);
-  r.g.a1 = sink;
-  if (global || sink >= r.g.lo) r.g.a1 = r.g.lo = 0;  // one run of visible tokens
+  r.g.lo = max(L - hp.window, 0);
+  r.g.a1 = hp.sink;
+  if (hp.global || hp.sink >= r.g.lo) r.g.a1 = r.g.lo = 0;  // one run of visible tokens
   r.g.b0 = (r.g.lo >> lp) << lp;
   r.g.n_a = (r.g.a1 + kDecodeTile - 1) / kDecodeTile;
   r.g.n = r.g.n_a + (int32_t)(((uint32_t)(L - r.g.b0) + kDecodeTile - 1) / kDecodeTile);
-  const int32_t n_all = (int32_t)(((uint32_t)L + last) >> lp);
-  r.n_sink = (int32_t)(((uint32_t)sink + last) >> lp);
-  r.w0 = (int32_t)(max((int64_t)L - lq - win + 1, (int64_t)0) >> lp);
-  if (global || r.w0 <= r.n_sink) r.n_sink = r.w0 = n_all;
   // A table that does not hold exactly these pages: the pair is reported and left out.
-  if (L > 0 && (r.len != r.n_sink + n_all - r.w0 || r.off < 0 || r.off > p.table_len - r.len)) {
+  if (L > 0 && (r.len != hp.total || r.off < 0 || r.off > p.table_len - r.len)) {
     report(p.status, 2);
     r.g.n = 0;
   }
@@ -897,13 +890,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 // Joins the chunks of the pairs that several CTAs shared: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
 // CTA c's last pair, if it goes on behind it, has n chunks: CTA c's second slot and the first slots of the n - 1 CTAs
 // after it. Block (c, head) joins them: each of its eight warps takes every eighth chunk, a lane D/32 columns, and the
-// warps' sums are added in order. The loads of four chunks a warp are in flight together with those of all the log
-// sums, so a pair of up to 32 chunks waits for memory twice (which pair, then its chunks), one of 148 five times.
+// warps' sums are added in order. The loads of five chunks a warp are in flight together with those of all the log
+// sums, so a pair of up to 40 chunks waits for memory twice (which pair, then its chunks), one of 148 five times.
 constexpr int kDecodeCombineWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kDecodeCombineWarps, 6) decode_combine_kernel(const DecodeParams p) {
-  constexpr int E = D / 32, NW = kDecodeCombineWarps, U = 4;
+__global__ void __launch_bounds__(32 * kDecodeCombineWarps, 5) decode_combine_kernel(const DecodeParams p) {
+  constexpr int E = D / 32, NW = kDecodeCombineWarps, U = 5;
   __shared__ float s_lse[kDecodeMaxCtas], s_sum[NW], s_top[NW], s_o[NW][D];
   const int32_t cta = blockIdx.x, head = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

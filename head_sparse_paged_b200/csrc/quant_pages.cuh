@@ -1,10 +1,13 @@
 // quant_pages.cuh -- the kernels that write 8-bit pages, append new rows to a pool, and read 8-bit pages back.
 //
 // All three move each byte once and are bound by HBM: 2 bytes read and 1 written per element (the write), or the
-// reverse (the read back). D/16 lanes share a row. In the two that quantise, lane c of a row holds its elements
-// 8c .. 8c+7 and D/2 + 8c .. D/2 + 8c+7, the pairs that the RoPE re-alignment rotates, so that the row's largest
-// magnitude is taken of the rotated bf16 values: a pool written here holds the quantised form of exactly the rows
-// that build_scatter_kernel would store.
+// reverse (the read back). A warp takes 16 rows of a page and issues all their loads before it uses the first: 8 KB (4 KB
+// for the read back) in flight a warp, and slices small enough to spread over all warps of the GPU. A whole page per
+// block, found by a binary search, left 2.5 us of dependent loads before each page's data and blocks with three pages
+// beside blocks with two: 4.1 TB/s on a batch of four 16-32K contexts.
+// In the kernels that quantise, lane c of a row holds its elements 8c .. 8c+7 and D/2 + 8c .. D/2 + 8c+7, the pairs that
+// the RoPE re-alignment rotates, so that the row's largest magnitude is taken of the rotated bf16 values: a pool written
+// here holds the quantised form of exactly the rows that build_scatter_kernel would store.
 #pragma once
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -15,6 +18,51 @@
 #include "rope.cuh"
 
 namespace segpaged {
+
+constexpr int kSliceRows = 16;  // rows of a page that one warp takes
+constexpr int kSliceWarps = 4;  // warps of a block
+
+// Pages of one (sequence, KV head) as storage_split gives them, with shifts for its divisions, from arrays that no host
+// check has seen: a negative length or sink counts as 0, a window below 1 as 1, fewer than min_q query rows as that.
+struct HeadPages {
+  int32_t L, sink, window, n_sink, w0, total;
+  bool global;
+  // logical page of table index t, and the table index of a logical page (-1: not kept)
+  __device__ __forceinline__ int32_t logical(int32_t t) const { return t < n_sink ? t : w0 + (t - n_sink); }
+  __device__ __forceinline__ int32_t index(int32_t lp) const { return lp < n_sink ? lp : lp < w0 ? -1 : lp - w0 + n_sink; }
+};
+
+__device__ __forceinline__ HeadPages head_pages(int32_t L, int32_t lq, const int32_t* cls, int32_t bk, int32_t log2_page) {
+  HeadPages r;
+  const int32_t last = (1 << log2_page) - 1;
+  r.L = max(L, 0);
+  r.global = cls[3 * bk] != 0;
+  r.sink = min(max(cls[3 * bk + 1], 0), r.L);
+  r.window = max(cls[3 * bk + 2], 1);
+  const int32_t n_all = (int32_t)(((uint32_t)r.L + last) >> log2_page);
+  r.n_sink = (int32_t)(((uint32_t)r.sink + last) >> log2_page);
+  r.w0 = (int32_t)(max((int64_t)r.L - lq - r.window + 1, (int64_t)0) >> log2_page);
+  if (r.global || r.w0 <= r.n_sink) r.n_sink = r.w0 = n_all;  // sink and window pages meet: everything is kept
+  r.total = r.n_sink + n_all - r.w0;
+  return r;
+}
+__device__ __forceinline__ HeadPages head_pages(const int32_t* ctx_len, const int32_t* q_len, const int32_t* cls, int32_t b,
+                                                int32_t bk, int32_t log2_page, int32_t min_q) {
+  return head_pages(ctx_len[b], max(q_len ? q_len[b] : 1, min_q), cls, bk, log2_page);
+}
+
+// Largest index i in [0, n) with start[i] <= x, for ascending starts and start[0] <= x: 32 of them a round.
+__device__ __forceinline__ int32_t warp_find(const int32_t* start, int32_t n, int64_t x) {
+  int32_t lo = 0;
+  while (n > 1) {
+    const int32_t step = (n + 31) >> 5, i = (threadIdx.x & 31) * step;
+    const bool le = i < n && start[lo + i] <= x;
+    const int32_t k = (__popc(__ballot_sync(0xffffffffu, le)) - 1) * step;
+    lo += k;
+    n = min(step, n - k);
+  }
+  return lo;
+}
 
 // One row's piece: elements 8c .. 8c+7 (lo) and D/2 + 8c .. (hi) of lane c.
 struct RowPiece {
@@ -48,80 +96,73 @@ struct BuildQuantParams {
   uint8_t* k_pool;     // [num_pages][P][D] codes
   uint8_t* v_pool;
   uint8_t* kv_scale;   // [num_pages][2][P] exponent bytes, K then V
+  int64_t table_len;
+  int32_t log2_page;
 };
 
 template <int D, int FMT, bool ROPE>
-__global__ void __launch_bounds__(256) build_quant_kernel(BuildQuantParams q) {
+__global__ void __launch_bounds__(32 * kSliceWarps) build_quant_kernel(BuildQuantParams q) {
   const BuildParams& p = q.b;
-  constexpr int LANES = D / 16;
-  constexpr int kPass = 256 / LANES;  // rows a pass of the block takes
-  const int nheads = p.B * p.Hkv;
-  const int64_t E = p.offs[nheads];
-  const int c = threadIdx.x % LANES;
-  for (int64_t e = blockIdx.x; e < E; e += gridDim.x) {
-    int lo = 0, hi = nheads;  // largest head with offs[head] <= e
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.offs[mid] <= e) lo = mid; else hi = mid;
-    }
-    const int bk = lo, b = bk / p.Hkv, kh = bk % p.Hkv;
-    const int32_t t = (int32_t)(e - p.offs[bk]);
-    const int32_t L = p.cu_k[b + 1] - p.cu_k[b];
-    const Split sp = storage_split(L, p.q_len[b], p.cls[3 * bk], p.cls[3 * bk + 1], p.cls[3 * bk + 2], p.P);
-    if (p.offs[bk + 1] - p.offs[bk] != sp.total) {
-      if (t == 0 && threadIdx.x == 0) report(p.status, 2);
-      if (t >= sp.total) continue;
-    }
-    const int32_t lp = t < sp.n_sink ? t : sp.w0 + (t - sp.n_sink);
+  constexpr int LANES = D / 16, ROWS = 32 / LANES, N = kSliceRows / ROWS;  // lanes of a row, rows a pass, passes
+  const int lane = threadIdx.x & 31, c = lane % LANES;
+  const int nheads = p.B * p.Hkv, log2_slices = q.log2_page - 4;
+  const int64_t slices = q.table_len << log2_slices, entries = p.offs[nheads];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && entries > q.table_len) report(p.status, 2);
+  const int64_t warps = (int64_t)gridDim.x * kSliceWarps;
+  for (int64_t x = (int64_t)blockIdx.x * kSliceWarps + (threadIdx.x >> 5); x < slices; x += warps) {
+    const int64_t e = x >> log2_slices;
+    const int32_t row0 = (int32_t)(x & ((1 << log2_slices) - 1)) * kSliceRows;
     const int32_t pid = p.table[e];
+    if (e >= entries) break;  // spare room behind the last table
+    const int bk = warp_find(p.offs, nheads, e), b = bk / p.Hkv, kh = bk - b * p.Hkv;
+    const int32_t t = (int32_t)(e - p.offs[bk]);
+    const int64_t src0 = p.cu_k[b];
+    const HeadPages hp = head_pages((int32_t)(p.cu_k[b + 1] - src0), max(p.q_len[b], 0), p.cls, bk, q.log2_page);
+    if (p.offs[bk + 1] - p.offs[bk] != hp.total) {
+      if (t == 0 && lane == 0) report(p.status, 2);
+      if (t >= hp.total) continue;
+    }
     if (pid < 0 || pid >= p.num_pages) {
-      if (threadIdx.x == 0) report(p.status, 1);
+      if (lane == 0) report(p.status, 1);
       continue;
     }
-    for (int row0 = 0; row0 < p.P; row0 += kPass) {
-      const int row = row0 + threadIdx.x / LANES;
-      const int64_t tok = (int64_t)lp * p.P + row;
-      RowPiece k, v;
-      k.lo = k.hi = v.lo = v.hi = make_uint4(0, 0, 0, 0);  // rows past the context end
-      if (row < p.P && tok < L) {
-        const int64_t src = ((p.cu_k[b] + tok) * p.Hkv + kh) * D + 8 * c;
-        k.lo = __ldg(reinterpret_cast<const uint4*>(p.k_dense + src));
-        k.hi = __ldg(reinterpret_cast<const uint4*>(p.k_dense + src + D / 2));
-        v.lo = __ldg(reinterpret_cast<const uint4*>(p.v_dense + src));
-        v.hi = __ldg(reinterpret_cast<const uint4*>(p.v_dense + src + D / 2));
-        if (ROPE) {
-          const float4* t4 = reinterpret_cast<const float4*>(p.cos_sin + (int64_t)b * D + 16 * c);
-          const float4 q0 = t4[0], q1 = t4[1], q2 = t4[2], q3 = t4[3];
-          RowPiece r;
-          r.lo.x = rot_pair(k.lo.x, k.hi.x, q0.x, q0.y, q0.z, q0.w, &r.hi.x);
-          r.lo.y = rot_pair(k.lo.y, k.hi.y, q1.x, q1.y, q1.z, q1.w, &r.hi.y);
-          r.lo.z = rot_pair(k.lo.z, k.hi.z, q2.x, q2.y, q2.z, q2.w, &r.hi.z);
-          r.lo.w = rot_pair(k.lo.w, k.hi.w, q3.x, q3.y, q3.z, q3.w, &r.hi.w);
-          k = r;
-        }
+    const int64_t tok0 = ((int64_t)hp.logical(t) << q.log2_page) + row0;
+    RowPiece k[N], v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      k[i].lo = k[i].hi = v[i].lo = v[i].hi = make_uint4(0, 0, 0, 0);  // rows past the context end
+      const int64_t tok = tok0 + i * ROWS + lane / LANES;
+      if (tok >= hp.L) continue;
+      const int64_t src = ((src0 + tok) * p.Hkv + kh) * D + 8 * c;
+      k[i].lo = __ldg(reinterpret_cast<const uint4*>(p.k_dense + src));
+      k[i].hi = __ldg(reinterpret_cast<const uint4*>(p.k_dense + src + D / 2));
+      v[i].lo = __ldg(reinterpret_cast<const uint4*>(p.v_dense + src));
+      v[i].hi = __ldg(reinterpret_cast<const uint4*>(p.v_dense + src + D / 2));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (ROPE) {  // (rows of zeros stay rows of zeros)
+        const float4* t4 = reinterpret_cast<const float4*>(p.cos_sin + (int64_t)b * D + 16 * c);
+        const float4 q0 = t4[0], q1 = t4[1], q2 = t4[2], q3 = t4[3];
+        RowPiece r;
+        r.lo.x = rot_pair(k[i].lo.x, k[i].hi.x, q0.x, q0.y, q0.z, q0.w, &r.hi.x);
+        r.lo.y = rot_pair(k[i].lo.y, k[i].hi.y, q1.x, q1.y, q1.z, q1.w, &r.hi.y);
+        r.lo.z = rot_pair(k[i].lo.z, k[i].hi.z, q2.x, q2.y, q2.z, q2.w, &r.hi.z);
+        r.lo.w = rot_pair(k[i].lo.w, k[i].hi.w, q3.x, q3.y, q3.z, q3.w, &r.hi.w);
+        k[i] = r;
       }
-      const int32_t ky = row_byte<FMT, LANES>(k), vy = row_byte<FMT, LANES>(v);
-      if (row >= p.P) continue;  // whole warps: kPass and P are multiples of a warp's rows or kPass > P >= 16
-      const int64_t at = ((int64_t)pid * p.P + row) * D;
-      store_codes<FMT>(q.k_pool + at, c, D / 2, k, ky);
-      store_codes<FMT>(q.v_pool + at, c, D / 2, v, vy);
+      const int32_t ky = row_byte<FMT, LANES>(k[i]), vy = row_byte<FMT, LANES>(v[i]);
+      const int32_t row = row0 + i * ROWS + lane / LANES;
+      const int64_t at = (((int64_t)pid << q.log2_page) + row) * D;
+      store_codes<FMT>(q.k_pool + at, c, D / 2, k[i], ky);
+      store_codes<FMT>(q.v_pool + at, c, D / 2, v[i], vy);
       if (c == 0) {
-        uint8_t* sc = q.kv_scale + (int64_t)pid * 2 * p.P + row;
+        uint8_t* sc = q.kv_scale + ((int64_t)pid << (q.log2_page + 1)) + row;
         sc[0] = (uint8_t)ky;
-        sc[p.P] = (uint8_t)vy;
+        sc[1 << q.log2_page] = (uint8_t)vy;
       }
     }
   }
-}
-
-// A sequence's geometry as the decode-side kernels read it from device memory: nothing there was checked on the
-// host, so lengths and classes are brought into range first.
-__device__ __forceinline__ Split device_split(const int32_t* ctx_len, const int32_t* q_len, const int32_t* cls, int b, int bk,
-                                              int32_t P, int32_t min_q, int32_t* L_out) {
-  const int32_t L = max(ctx_len[b], 0);
-  const int32_t lq = max(q_len ? q_len[b] : 1, min_q);
-  *L_out = L;
-  return storage_split(L, lq, cls[3 * bk], max(cls[3 * bk + 1], 0), max(cls[3 * bk + 2], 1), P);
 }
 
 struct AppendParams {
@@ -138,43 +179,36 @@ struct AppendParams {
   uint8_t* kv_scale;           // null for bf16 pools
   int32_t* status;
   int64_t table_len;
-  int32_t total_new, B, Hkv, P, num_pages;
+  int32_t total_new, B, Hkv, log2_page, num_pages;
 };
 
-// One group of D/16 lanes per (new row, KV head), both its K and its V.
+// A warp per 32 / (D/16) KV heads of one new row, both its K and its V: the search for the row's sequence is the warp's.
 template <int D, int FMT>
-__global__ void __launch_bounds__(128) append_kernel(AppendParams p) {
-  constexpr int LANES = D / 16;
-  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES;
-  const int c = threadIdx.x % LANES;
-  bool ok = item < (int64_t)p.total_new * p.Hkv;
-  const int32_t r = ok ? (int32_t)(item / p.Hkv) : 0;
-  const int kh = ok ? (int)(item % p.Hkv) : 0;
+__global__ void __launch_bounds__(32) append_kernel(AppendParams p) {
+  constexpr int LANES = D / 16, HEADS = 32 / LANES;
+  const int32_t r = (int32_t)blockIdx.x, lane = threadIdx.x, c = lane % LANES;
+  const int32_t kh = (int32_t)blockIdx.y * HEADS + lane / LANES;
+  bool ok = kh < p.Hkv;
   RowPiece k, v;
   k.lo = k.hi = v.lo = v.hi = make_uint4(0, 0, 0, 0);
   if (ok) {  // issued before the page look-up, whose loads depend on one another
-    const int64_t src = item * D + 8 * c;
+    const int64_t src = ((int64_t)r * p.Hkv + kh) * D + 8 * c;
     k.lo = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
     k.hi = __ldg(reinterpret_cast<const uint4*>(p.k_new + src + D / 2));
     v.lo = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
     v.hi = __ldg(reinterpret_cast<const uint4*>(p.v_new + src + D / 2));
   }
-  ok = ok && r >= p.cu_new[0] && r < p.cu_new[p.B];  // rows outside every sequence are left alone
+  const int32_t first = p.cu_new[0], end = p.cu_new[p.B];
+  if (r < first || r >= end) return;  // rows outside every sequence are left alone (the whole warp's row)
+  const int32_t b = warp_find(p.cu_new, p.B, r);
   int64_t at = 0, sat = 0;
   if (ok) {
-    int lo = 0, hi = p.B;  // last sequence that starts at or before r
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.cu_new[mid] <= r) lo = mid; else hi = mid;
-    }
-    const int b = lo, bk = b * p.Hkv + kh;
-    int32_t L;
-    const Split sp = device_split(p.ctx_len, p.q_len, p.cls, b, bk, p.P, 0, &L);
-    const int64_t pos = (int64_t)L - p.cu_new[b + 1] + r;
+    const int32_t bk = b * p.Hkv + kh;
     const int64_t off = p.offs[bk], n = (int64_t)p.offs[bk + 1] - off;
-    const int32_t lp = (int32_t)(pos / p.P), row = (int32_t)(pos % p.P);
-    const int32_t t = lp < sp.n_sink ? lp : lp < sp.w0 ? -1 : lp - sp.w0 + sp.n_sink;
-    bool fits = pos >= 0 && n == sp.total;
+    const HeadPages hp = head_pages(p.ctx_len, p.q_len, p.cls, b, bk, p.log2_page, 0);
+    const int64_t pos = (int64_t)hp.L - p.cu_new[b + 1] + r;
+    const int32_t row = (int32_t)(pos & ((1 << p.log2_page) - 1)), t = hp.index((int32_t)(pos >> p.log2_page));
+    bool fits = pos >= 0 && n == hp.total;
     ok = pos >= 0 && t >= 0;  // t < 0: a page this head does not keep
     if (ok && (t >= n || off < 0 || off + t >= p.table_len)) ok = fits = false;
     if (!fits && c == 0) report(p.status, 2);
@@ -184,8 +218,8 @@ __global__ void __launch_bounds__(128) append_kernel(AppendParams p) {
         if (c == 0) report(p.status, 1);
         ok = false;
       }
-      at = ((int64_t)pid * p.P + row) * D;
-      sat = (int64_t)pid * 2 * p.P + row;
+      at = (((int64_t)pid << p.log2_page) + row) * D;
+      sat = ((int64_t)pid << (p.log2_page + 1)) + row;
     }
   }
   if (FMT == kFmtBf16) {
@@ -204,7 +238,7 @@ __global__ void __launch_bounds__(128) append_kernel(AppendParams p) {
   store_codes<FMT>(p.v_pool + at, c, D / 2, v, vy);
   if (c == 0) {
     p.kv_scale[sat] = (uint8_t)ky;
-    p.kv_scale[sat + p.P] = (uint8_t)vy;
+    p.kv_scale[sat + (1 << p.log2_page)] = (uint8_t)vy;
   }
 }
 
@@ -221,16 +255,17 @@ struct DequantParams {
   __nv_bfloat16* v_out;
   int32_t* status;
   int64_t table_len;
-  int32_t B, Hkv, P, num_pages;
+  int32_t B, Hkv, log2_page, num_pages;
 };
 
-// Sixteen codes (one 16-byte load) as bf16: code * 2^(y - 127) rounded to nearest even. e4m3 has 4 and int8 7
-// significant bits, so only results below the bf16 normal range round at all.
+// Eight codes as bf16: code * 2^(y - 127) rounded to nearest even. e4m3 has 4 and int8 7 significant bits, so only
+// results below the bf16 normal range round at all.
 template <int FMT>
-__device__ __forceinline__ void dequant16(uint4 w, float scale, uint32_t (&o)[8]) {
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ uint4 dequant8(uint2 w, float scale) {
+  const uint32_t in[2] = {w.x, w.y};
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     uint32_t h[2];
     codes_to_half2x2<FMT, false>(in[i], h[0], h[1]);
 #pragma unroll
@@ -240,51 +275,53 @@ __device__ __forceinline__ void dequant16(uint4 w, float scale, uint32_t (&o)[8]
       o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&r);
     }
   }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// D/8 lanes a row: 8-byte loads and 16-byte stores, both contiguous over the lanes.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256) dequant_pages_kernel(DequantParams p) {
-  constexpr int LANES = D / 16;
-  const int nheads = p.B * p.Hkv;
-  const int64_t E = min((int64_t)p.offs[nheads], p.table_len);
-  const int c = threadIdx.x % LANES;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && p.offs[nheads] > p.table_len) report(p.status, 2);
-  for (int64_t e = blockIdx.x; e < E; e += gridDim.x) {
-    int lo = 0, hi = nheads;  // largest head with offs[head] <= e
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.offs[mid] <= e) lo = mid; else hi = mid;
-    }
-    const int bk = lo;
-    const int32_t t = (int32_t)(e - p.offs[bk]);
-    int32_t L;
-    const Split sp = device_split(p.ctx_len, p.q_len, p.cls, bk / p.Hkv, bk, p.P, 0, &L);
-    if (p.offs[bk + 1] - p.offs[bk] != sp.total) {
-      if (t == 0 && threadIdx.x == 0) report(p.status, 2);
-      if (t >= sp.total) continue;
-    }
-    const int32_t lp = t < sp.n_sink ? t : sp.w0 + (t - sp.n_sink);
+__global__ void __launch_bounds__(32 * kSliceWarps) dequant_pages_kernel(DequantParams p) {
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, N = kSliceRows / ROWS;
+  const int lane = threadIdx.x & 31, c = lane % LANES;
+  const int nheads = p.B * p.Hkv, log2_slices = p.log2_page - 4;
+  const int64_t slices = p.table_len << log2_slices, entries = p.offs[nheads];
+  const int64_t warps = (int64_t)gridDim.x * kSliceWarps;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && entries > p.table_len) report(p.status, 2);
+  for (int64_t x = (int64_t)blockIdx.x * kSliceWarps + (threadIdx.x >> 5); x < slices; x += warps) {
+    const int64_t e = x >> log2_slices;
+    const int32_t row0 = (int32_t)(x & ((1 << log2_slices) - 1)) * kSliceRows;
     const int32_t pid = p.table[e];
+    if (e >= entries) break;  // spare room behind the last table
     if (pid < 0 || pid >= p.num_pages) {
-      if (threadIdx.x == 0) report(p.status, 1);
+      if (lane == 0) report(p.status, 1);
       continue;
     }
-    for (int row = threadIdx.x / LANES; row < p.P; row += 256 / LANES) {
-      const int64_t at = ((int64_t)pid * p.P + row) * D + 16 * c;
-      uint32_t k[8] = {}, v[8] = {};
-      if ((int64_t)lp * p.P + row < L) {
-        const uint8_t* sc = p.kv_scale + (int64_t)pid * 2 * p.P + row;
-        const uint4 kw = __ldg(reinterpret_cast<const uint4*>(p.k_pool + at));
-        const uint4 vw = __ldg(reinterpret_cast<const uint4*>(p.v_pool + at));
-        dequant16<FMT>(kw, row_scale(__ldg(sc)), k);
-        dequant16<FMT>(vw, row_scale(__ldg(sc + p.P)), v);
-      }
-      uint4* ko = reinterpret_cast<uint4*>(p.k_out + at);
-      uint4* vo = reinterpret_cast<uint4*>(p.v_out + at);
-      ko[0] = make_uint4(k[0], k[1], k[2], k[3]);
-      ko[1] = make_uint4(k[4], k[5], k[6], k[7]);
-      vo[0] = make_uint4(v[0], v[1], v[2], v[3]);
-      vo[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    // the codes are on their way while the head they belong to, and with it the context's end, is looked up
+    const int64_t at = (((int64_t)pid << p.log2_page) + row0 + lane / LANES) * D + 8 * c;
+    const uint8_t* sc = p.kv_scale + ((int64_t)pid << (p.log2_page + 1)) + row0 + lane / LANES;
+    uint2 k[N], v[N];
+    int32_t ky[N], vy[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      k[i] = __ldg(reinterpret_cast<const uint2*>(p.k_pool + at + i * ROWS * D));
+      v[i] = __ldg(reinterpret_cast<const uint2*>(p.v_pool + at + i * ROWS * D));
+      ky[i] = __ldg(sc + i * ROWS);
+      vy[i] = __ldg(sc + i * ROWS + (1 << p.log2_page));
+    }
+    const int bk = warp_find(p.offs, nheads, e), b = bk / p.Hkv;
+    const int32_t t = (int32_t)(e - p.offs[bk]);
+    const HeadPages hp = head_pages(p.ctx_len, p.q_len, p.cls, b, bk, p.log2_page, 0);
+    if (p.offs[bk + 1] - p.offs[bk] != hp.total) {
+      if (t == 0 && lane == 0) report(p.status, 2);
+      if (t >= hp.total) continue;
+    }
+    const int64_t tok0 = ((int64_t)hp.logical(t) << p.log2_page) + row0 + lane / LANES;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool in = tok0 + i * ROWS < hp.L;  // rows past the context end are written as zero
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(p.k_out + at + i * ROWS * D) = in ? dequant8<FMT>(k[i], row_scale(ky[i])) : zero;
+      *reinterpret_cast<uint4*>(p.v_out + at + i * ROWS * D) = in ? dequant8<FMT>(v[i], row_scale(vy[i])) : zero;
     }
   }
 }

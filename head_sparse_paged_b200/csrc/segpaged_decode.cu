@@ -44,16 +44,21 @@ int sm_count() {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA; }
 
+// Blocks of the kernels that take 16 rows of a page a warp: a warp for each slice (the kernels loop past the limit).
+int slice_blocks(int64_t table_len, int log2_page) {
+  const int64_t per_page = (1 << log2_page) / kSliceRows;
+  return (int)std::min<int64_t>(ceil_div(std::min<int64_t>(table_len, INT32_MAX) * per_page, kSliceWarps), 1 << 22);
+}
+
 template <int D, int FMT>
 void launch_build_quant(const BuildQuantParams& p, int grid, cudaStream_t st) {
-  if (p.b.cos_sin) build_quant_kernel<D, FMT, true><<<grid, 256, 0, st>>>(p);
-  else build_quant_kernel<D, FMT, false><<<grid, 256, 0, st>>>(p);
+  if (p.b.cos_sin) build_quant_kernel<D, FMT, true><<<grid, 32 * kSliceWarps, 0, st>>>(p);
+  else build_quant_kernel<D, FMT, false><<<grid, 32 * kSliceWarps, 0, st>>>(p);
 }
 
 template <int D, int FMT>
 void launch_append(const AppendParams& p, cudaStream_t st) {
-  const int64_t lanes = (int64_t)p.total_new * p.Hkv * (D / 16);
-  append_kernel<D, FMT><<<(unsigned)ceil_div(lanes, 128), 128, 0, st>>>(p);
+  append_kernel<D, FMT><<<dim3(p.total_new, (unsigned)ceil_div(p.Hkv, 512 / D)), 32, 0, st>>>(p);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -147,15 +152,15 @@ int launch_decode(const void* k_pool, const void* v_pool, const DecodeParams& p,
 
 extern "C" int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format, const void* k_dense, const void* v_dense,
                                  const int32_t* cu_seqlens_k, const int32_t* q_len, const segpaged_head_class* cls,
-                                 const int32_t* page_table, const int32_t* page_table_offs, const float* rope_cos_sin,
-                                 void* k_pool, void* v_pool, uint8_t* kv_scale, int32_t* status, void* stream) {
+                                    const int32_t* page_table, int64_t page_table_len, const int32_t* page_table_offs,
+                                    const float* rope_cos_sin, void* k_pool, void* v_pool, uint8_t* kv_scale,
+                                    int32_t* status, void* stream) {
   const int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
   if (rc) return rc;
-  if (dims->num_seqs == 0) return SEGPAGED_OK;
+  if (page_table_len < 0) return SEGPAGED_ERR_DIMS;
+  if (dims->num_seqs == 0 || page_table_len == 0) return SEGPAGED_OK;
   if (!k_dense || !v_dense || !cu_seqlens_k || !q_len || !cls || !page_table || !page_table_offs) return SEGPAGED_ERR_NULL;
   if (!aligned16(k_dense) || !aligned16(v_dense) || (rope_cos_sin && !aligned16(rope_cos_sin))) return SEGPAGED_ERR_ALIGN;
-  const int sms = sm_count();
-  if (sms <= 0) return SEGPAGED_ERR_CUDA;
   BuildQuantParams p;
   p.b.k_dense = static_cast<const __nv_bfloat16*>(k_dense);
   p.b.v_dense = static_cast<const __nv_bfloat16*>(v_dense);
@@ -175,8 +180,10 @@ extern "C" int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format
   p.k_pool = static_cast<uint8_t*>(k_pool);
   p.v_pool = static_cast<uint8_t*>(v_pool);
   p.kv_scale = kv_scale;
+  p.table_len = page_table_len;
+  p.log2_page = log2_int(dims->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SEGPAGED_BY_SHAPE_8BIT(launch_build_quant, (p, sms * 8, st));
+  SEGPAGED_BY_SHAPE_8BIT(launch_build_quant, (p, slice_blocks(page_table_len, p.log2_page), st));
   return launched();
 }
 
@@ -191,7 +198,7 @@ extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, con
   if (dims->num_seqs == 0 || total_new == 0) return SEGPAGED_OK;
   if (!k_new || !v_new || !cu_seqlens_new || !ctx_len || !cls || (!page_table && page_table_len > 0) || !page_table_offs) return SEGPAGED_ERR_NULL;
   if (!aligned16(k_new) || !aligned16(v_new)) return SEGPAGED_ERR_ALIGN;
-  if (ceil_div((int64_t)total_new * dims->num_kv_heads * (dims->head_dim / 16), 128) > INT32_MAX) return SEGPAGED_ERR_DIMS;
+  if (ceil_div(dims->num_kv_heads, 512 / dims->head_dim) > 65535) return SEGPAGED_ERR_DIMS;  // the grid's second extent
   AppendParams p;
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
   p.v_new = static_cast<const __nv_bfloat16*>(v_new);
@@ -209,7 +216,7 @@ extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, con
   p.total_new = total_new;
   p.B = dims->num_seqs;
   p.Hkv = dims->num_kv_heads;
-  p.P = dims->page_size;
+  p.log2_page = log2_int(dims->page_size);
   p.num_pages = dims->num_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   SEGPAGED_BY_SHAPE(launch_append, (p, st));
@@ -219,7 +226,7 @@ extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, con
 namespace {
 template <int D, int FMT>
 void launch_dequant(const DequantParams& p, int grid, cudaStream_t st) {
-  dequant_pages_kernel<D, FMT><<<grid, 256, 0, st>>>(p);
+  dequant_pages_kernel<D, FMT><<<grid, 32 * kSliceWarps, 0, st>>>(p);
 }
 }  // namespace
 
@@ -231,11 +238,9 @@ extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_form
   const int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
   if (rc) return rc;
   if (page_table_len < 0) return SEGPAGED_ERR_DIMS;
-  if (dims->num_seqs == 0) return SEGPAGED_OK;
-  if (!ctx_len || !cls || (!page_table && page_table_len > 0) || !page_table_offs || !k_out || !v_out) return SEGPAGED_ERR_NULL;
+  if (dims->num_seqs == 0 || page_table_len == 0) return SEGPAGED_OK;
+  if (!ctx_len || !cls || !page_table || !page_table_offs || !k_out || !v_out) return SEGPAGED_ERR_NULL;
   if (!aligned16(k_out) || !aligned16(v_out)) return SEGPAGED_ERR_ALIGN;
-  const int sms = sm_count();
-  if (sms <= 0) return SEGPAGED_ERR_CUDA;
   DequantParams p;
   p.ctx_len = ctx_len;
   p.q_len = q_len;
@@ -251,10 +256,10 @@ extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_form
   p.table_len = page_table_len;
   p.B = dims->num_seqs;
   p.Hkv = dims->num_kv_heads;
-  p.P = dims->page_size;
+  p.log2_page = log2_int(dims->page_size);
   p.num_pages = dims->num_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SEGPAGED_BY_SHAPE_8BIT(launch_dequant, (p, sms * 8, st));
+  SEGPAGED_BY_SHAPE_8BIT(launch_dequant, (p, slice_blocks(page_table_len, p.log2_page), st));
   return launched();
 }
 

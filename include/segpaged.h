@@ -406,9 +406,10 @@ int segpaged_select_topk(int32_t num_seqs, const float* mass, const int32_t* cu_
  * their exponent bytes, are not touched. Returns SEGPAGED_ERR_FORMAT for SEGPAGED_KV_BF16.
  */
 int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format, const void* k_dense, const void* v_dense,
-                      const int32_t* cu_seqlens_k, const int32_t* q_len, const segpaged_head_class* cls,
-                      const int32_t* page_table, const int32_t* page_table_offs, const float* rope_cos_sin,
-                      void* k_pool, void* v_pool, uint8_t* kv_scale, int32_t* status, void* stream);
+                           const int32_t* cu_seqlens_k, const int32_t* q_len, const segpaged_head_class* cls,
+                           const int32_t* page_table, int64_t page_table_len, const int32_t* page_table_offs,
+                           const float* rope_cos_sin, void* k_pool, void* v_pool, uint8_t* kv_scale, int32_t* status,
+                           void* stream);
 
 /*
  * Writes the new tokens' keys and values into their pages (one kernel launch), quantised for an 8-bit pool

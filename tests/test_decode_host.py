@@ -71,8 +71,8 @@ def _call(name, dims=None, **change):
     """The C call `name` with plausible arguments, `change` replacing some: refused before any device work."""
     d = (dims or sp.Dims(2, 8, 2, 64, 16, 10)).c()
     order = {
-        "segpaged_build_quant": ["fmt", "k_dense", "v_dense", "cu_k", "q_len", "cls", "table", "offs", "rope", "k", "v", "sc",
-                                 "status", "stream"],
+        "segpaged_build_quant": ["fmt", "k_dense", "v_dense", "cu_k", "q_len", "cls", "table", "tlen", "offs", "rope", "k", "v",
+                                 "sc", "status", "stream"],
         "segpaged_append": ["fmt", "k_new", "v_new", "n", "cu", "ctx", "q_len", "cls", "table", "tlen", "offs", "k", "v", "sc",
                             "status", "stream"],
         "segpaged_pages_dequant": ["fmt", "ctx", "q_len", "cls", "table", "tlen", "offs", "k", "v", "sc", "ko", "vo", "status",
