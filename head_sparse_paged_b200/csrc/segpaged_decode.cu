@@ -44,7 +44,7 @@ int sm_count() {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA; }
 
-// Blocks of the kernels that take 16 rows of a page a warp: a warp for each slice (the kernels loop past the limit).
+// Blocks of the kernels that take a slice of a page a warp: a warp for each slice (the kernels loop past the limit).
 int slice_blocks(int64_t table_len, int log2_page) {
   const int64_t per_page = (1 << log2_page) / kSliceRows;
   return (int)std::min<int64_t>(ceil_div(std::min<int64_t>(table_len, INT32_MAX) * per_page, kSliceWarps), 1 << 22);

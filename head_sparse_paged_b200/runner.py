@@ -318,6 +318,129 @@ class Runner:
             raise RuntimeError(f"device status word {s:#x}")
 
 
+KV_DTYPES = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+class Decoder:
+    """The decode steps that follow a Runner's prefill: one new token per sequence and step, in pools of its own.
+
+    kv: the pools' format ("bf16", "e4m3", "int8"); they are built from the runner's dense K/V (keep_dense) with
+    segpaged_build or segpaged_build_quant. max_new: the most tokens a sequence grows by. Context length and query length
+    are counted up together per token, so a head's page table only ever grows at its end, by a page when a sequence
+    crosses a page boundary; until then a step touches nothing but the device arrays of lengths.
+    graphs: replay each layer's append and attention as one CUDA graph, captured after its first direct run.
+    """
+
+    def __init__(self, r: Runner, max_new: int, kv: str = "bf16", graphs: bool = False):
+        if r.append or r.frags is not None:
+            raise ValueError("decoding starts from a plain runner (keys re-aligned when they are built, or not at all)")
+        w = r.w
+        self.r, self.w, self.max_new, self.kv, self.graphs = r, w, int(max_new), kv, graphs
+        self.dtype = KV_DTYPES[kv]
+        dev, B, H, D, P = r.device, w.num_seqs, w.num_kv_heads, w.head_dim, w.page_size
+        self.ctx, self.ql = r.ctx.copy(), r.ql.copy()
+        grow = -(-self.max_new // P) + 1                       # pages a head may need on top of its prefill's
+        need = sum(int(r.state[li].pages_per_head.sum()) for li in r.layers) + len(r.layers) * B * H * grow
+        self.dims = sp.Dims(B, w.num_q_heads, H, D, P, max(need, 1))
+        self.free = np.random.default_rng(w.seed).permutation(self.dims.num_pages).astype(np.int32)
+        self.taken = 0
+        raw = torch.bfloat16 if kv == "bf16" else torch.uint8
+        self.k_pool, self.v_pool = (torch.zeros(self.dims.num_pages, P, D, dtype=raw, device=dev).view(self.dtype)
+                                    for _ in range(2))
+        self.kv_scale = None if kv == "bf16" else torch.zeros(self.dims.num_pages, 2, P, dtype=torch.uint8, device=dev)
+        self.ctx_dev = torch.from_numpy(self.ctx).to(dev)
+        self.ql_dev = torch.from_numpy(self.ql).to(dev)
+        self.cu_new = torch.arange(B + 1, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.workspace = torch.empty(sp.segpaged_decode_workspace_bytes(self.dims), dtype=torch.uint8, device=dev)
+        self.pages, self.table_dev, self.offs_dev, self.io, self._calls = {}, {}, {}, {}, {}
+        for li in r.layers:
+            per = r.state[li].pages_per_head
+            self.pages[li] = [list(self._take(int(n))) for n in per]
+            self.table_dev[li] = torch.zeros(int(per.sum()) + B * H * grow, dtype=torch.int32, device=dev)
+            self.offs_dev[li] = torch.zeros(B * H + 1, dtype=torch.int32, device=dev)
+            self._upload_table(li)
+            k, v = r.dense_of(li)
+            cls = r.state[li].cls_dev
+            build = ((sp.segpaged_build, (self.k_pool, self.v_pool)) if kv == "bf16" else
+                     (sp.segpaged_build_quant, (self.k_pool, self.v_pool, self.kv_scale)))
+            build[0](self.dims, k, v, r.cu_k_dev, self.ql_dev, cls, self.table_dev[li], self.offs_dev[li], r.rope, *build[1],
+                     self.status)
+            bf = dict(dtype=torch.bfloat16, device=dev)
+            q, o = torch.zeros(B, w.num_q_heads, D, **bf), torch.zeros(B, w.num_q_heads, D, **bf)
+            kn, vn = torch.zeros(B, H, D, **bf), torch.zeros(B, H, D, **bf)
+            lse = torch.zeros(w.num_q_heads, B, dtype=torch.float32, device=dev)
+            self.io[li] = (q, kn, vn, o, lse)
+            seq = (self.ctx_dev, self.ql_dev, cls)
+            tab = (self.table_dev[li], self.offs_dev[li])
+            pools = (self.k_pool, self.v_pool, self.kv_scale)
+            self._calls[li] = [sp.prepare_append(self.dims, kn, vn, self.cu_new, *seq, *tab, *pools, self.status),
+                               sp.prepare_attn_decode(self.dims, q, *pools, *tab, *seq, r.scale, o, lse, self.workspace,
+                                                      self.status), None]
+
+    def _take(self, n):
+        ids = self.free[self.taken:self.taken + n]
+        if len(ids) < n:
+            raise RuntimeError("the decode pool is out of pages")
+        self.taken += n
+        return ids
+
+    def _upload_table(self, li):
+        flat = np.array([p for head in self.pages[li] for p in head], np.int32)
+        offs = np.concatenate([[0], np.cumsum([len(head) for head in self.pages[li]])]).astype(np.int32)
+        self.table_dev[li][:len(flat)].copy_(torch.from_numpy(flat))
+        self.offs_dev[li].copy_(torch.from_numpy(offs))
+
+    def advance(self):
+        """Makes room for one more token per sequence; call once before the layers' steps."""
+        if int(self.ctx[0] - self.r.ctx[0]) >= self.max_new:
+            raise RuntimeError(f"the decoder was set up for {self.max_new} new tokens")
+        self.ctx += 1
+        self.ql += 1
+        self.ctx_dev += 1
+        self.ql_dev += 1
+        if not np.any((self.ctx - 1) % self.w.page_size == 0):
+            return
+        for li in self.r.layers:
+            per = sp.segpaged_pages_bytes(self.dims, self.ctx, self.ql, self.r.state[li].cls)[2]
+            for head, n in zip(self.pages[li], per):
+                head.extend(self._take(int(n) - len(head)))
+            self._upload_table(li)
+
+    def step(self, li, q, k_new, v_new, stream=None):
+        """Layer li's attention of the new tokens: q [B, Hq, D], k_new and v_new [B, Hkv, D] bf16 (RoPE included).
+        Returns O [B, Hq, D] bf16 and LSE [Hq, B], buffers that the layer's next step overwrites."""
+        qb, kb, vb, o, lse = self.io[li]
+        s = torch.cuda.current_stream(self.r.device) if stream is None else stream
+        append, attend, graph = self._calls[li]
+        with torch.cuda.stream(s):
+            qb.copy_(q)
+            kb.copy_(k_new)
+            vb.copy_(v_new)
+            if graph is not None:
+                graph.replay()
+                return o, lse
+        append(s)
+        attend(s)
+        if self.graphs:
+            def both(st):
+                append(st)
+                attend(st)
+            self._calls[li][2] = capture_graph(both, self.r.device)
+        return o, lse
+
+    def read_back(self, li, k_out, v_out, stream=None):
+        """The layer's stored pages of an 8-bit pool as bf16 pages of the same ids (for a prefill over them)."""
+        sp.segpaged_pages_dequant(self.dims, self.ctx_dev, self.ql_dev, self.r.state[li].cls_dev, self.table_dev[li],
+                                  self.offs_dev[li], self.k_pool, self.v_pool, self.kv_scale, k_out, v_out, self.status,
+                                  stream)
+
+    def check_status(self):
+        s = int(self.status.item())
+        if s:
+            raise RuntimeError(f"device status word {s:#x}")
+
+
 def capture_graph(call, device) -> torch.cuda.CUDAGraph:
     """A CUDA graph of one prepared C-ABI call that has already run once on `device` (the library configures
     a kernel on its first launch on a device, which must not happen inside a capture). Capturing launches
@@ -347,10 +470,13 @@ def main(argv=None):
     ap.add_argument("workload")
     ap.add_argument("--layers", default="0", help="comma-separated layer indices")
     ap.add_argument("--launches", type=int, default=2, help="prefill launches per layer")
+    ap.add_argument("--decode", type=int, default=0, metavar="N",
+                    help="decode N tokens per sequence after the prefill and print the time of a layer's step")
+    ap.add_argument("--kv", choices=sorted(KV_DTYPES), default="bf16", help="format of the pools that are decoded from")
     args = ap.parse_args(argv)
     w = synth.get(args.workload)
     layers = [int(x) for x in args.layers.split(",")]
-    r = Runner(w, layers=layers)
+    r = Runner(w, layers=layers, keep_dense=args.decode > 0)
     torch.cuda.synchronize()
     for _ in range(args.launches):
         for li in layers:
@@ -359,6 +485,26 @@ def main(argv=None):
     r.check_status()
     print(f"{w.name}: layers {layers}, {args.launches} prefill launches each, pool {r.num_pages} pages, "
           f"{torch.cuda.max_memory_allocated() / 1e9:.2f} GB peak device memory")
+    if args.decode > 0:
+        d = Decoder(r, args.decode, args.kv, graphs=True)
+        gen = torch.Generator(device=r.device)
+        gen.manual_seed(w.seed)
+        new = [torch.randn(s, generator=gen, device=r.device).to(torch.bfloat16)
+               for s in ((w.num_seqs, w.num_q_heads, w.head_dim), *[(w.num_seqs, w.num_kv_heads, w.head_dim)] * 2)]
+        times = []
+        for _ in range(args.decode):
+            d.advance()
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for li in layers:
+                d.step(li, *new)
+            end.record()
+            times.append((start, end))
+        torch.cuda.synchronize()
+        d.check_status()
+        us = sorted(a.elapsed_time(b) * 1e3 / len(layers) for a, b in times[1:] or times)
+        print(f"decode: {args.decode} tokens x {w.num_seqs} sequences from {args.kv} pools, {us[len(us) // 2]:.1f} us a layer "
+              f"and step (append and attention, inputs copied in)")
     return 0
 
 
