@@ -254,11 +254,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   const int32_t u_lo = min((int32_t)threadIdx.x * per, pairs), u_hi = min(u_lo + per, pairs);
   DecodePair own = {};
   int32_t mine = 0;  // the tiles are fewer than the entries of the page table
-  if (per == 1) {
-    if (u_lo < u_hi) own = decode_pair(p, u_lo);
-    mine = own.g.n;
-  } else {
-    for (int32_t u = u_lo; u < u_hi; ++u) mine += decode_pair(p, u).g.n;
+  // (The kernel runs most of its code once per launch, so its size is time: loops over pairs stay rolled.)
+#pragma unroll 1
+  for (int32_t u = u_lo; u < u_hi; ++u) {
+    own = decode_pair(p, u);
+    mine += own.g.n;
   }
   int32_t incl = mine;
 #pragma unroll
@@ -281,36 +281,35 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   const uint32_t share = units / ctas, spare = units - share * ctas;  // the first `spare` CTAs take one unit more
   const bool takes_part = cta < (int32_t)ctas;
   const uint32_t lo_unit = share * cta + min((uint32_t)cta, spare), hi_unit = lo_unit + share + ((uint32_t)cta < spare);
-  if (takes_part) {
-    int32_t rank = before;
-    for (int32_t u = u_lo; u < u_hi; ++u) {
-      const int32_t n = per == 1 ? own.g.n : decode_pair(p, u).g.n;
-      const uint32_t at = 2u * rank + (uint32_t)C::PAIR_COST * u, next = at + 2u * n + C::PAIR_COST;
-      if (lo_unit >= at && lo_unit < next) {
-        const int32_t tile = min(n, (int32_t)(lo_unit - at + 1) / 2);
-        sm.pair0 = u;
-        sm.tile0 = tile;
-        sm.first_rank = rank + tile;
-        if (per == 1 && tile < n) {  // the run's first page ids will be wanted in a moment
-          const int64_t tok = tile < own.g.n_a ? (int64_t)tile * kDecodeTile
-                                               : own.g.b0 + (int64_t)(tile - own.g.n_a) * kDecodeTile;
-          const int32_t page = (int32_t)(tok >> p.log2_page);
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + own.off + (page < own.n_sink ? page : page - own.w0 + own.n_sink)));
-        }
-      }
-      if (hi_unit > at && hi_unit <= next) sm.end_rank = rank + min(n, (int32_t)(hi_unit - at + 1) / 2);
-      rank += n;
-    }
-  }
-  // pairs without a visible key (an empty sequence): O = 0, LSE = -inf, written by one CTA each
   const int32_t heads = min(p.G, kDecodeGroup), Hq = p.Hkv * p.G;
+  int32_t rank = before;
+#pragma unroll 1
   for (int32_t u = u_lo; u < u_hi; ++u) {
-    if (per == 1 ? own.g.L > 0 : p.ctx_len[(u >> p.log2_hg) / p.Hkv] > 0) continue;
-    if (u % (int32_t)gridDim.x != cta) continue;
-    const DecodePair e = decode_pair(p, u);
-    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)e.b * Hq + e.h0) * D);
-    for (int i = 0; i < heads * D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
-    for (int h = 0; h < heads; ++h) p.lse[(int64_t)(e.h0 + h) * p.B + e.b] = -INFINITY;
+    if (per > 1) own = decode_pair(p, u);
+    const int32_t n = own.g.n;
+    const uint32_t at = 2u * rank + (uint32_t)C::PAIR_COST * u, next = at + 2u * n + C::PAIR_COST;
+    if (takes_part && lo_unit >= at && lo_unit < next) {
+      const int32_t tile = min(n, (int32_t)(lo_unit - at + 1) / 2);
+      sm.pair0 = u;
+      sm.tile0 = tile;
+      sm.first_rank = rank + tile;
+      if (tile < n) {  // the run's first page ids will be wanted in a moment
+        const int64_t tok = tile < own.g.n_a ? (int64_t)tile * kDecodeTile
+                                             : own.g.b0 + (int64_t)(tile - own.g.n_a) * kDecodeTile;
+        const int32_t page = (int32_t)(tok >> p.log2_page);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + own.off + (page < own.n_sink ? page : page - own.w0 + own.n_sink)));
+      }
+    }
+    if (takes_part && hi_unit > at && hi_unit <= next) sm.end_rank = rank + min(n, (int32_t)(hi_unit - at + 1) / 2);
+    rank += n;
+    // a pair without a visible key (an empty sequence): O = 0, LSE = -inf, written by one CTA
+    if (own.g.L == 0 && u % gridDim.x == cta) {
+      uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)own.b * Hq + own.h0) * D);
+#pragma unroll 1
+      for (int i = 0; i < heads * D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+      for (int h = 0; h < heads; ++h) p.lse[(int64_t)(own.h0 + h) * p.B + own.b] = -INFINITY;
+    }
   }
   if (threadIdx.x == 0) {
     p.part_meta[2 * cta] = 0;
@@ -338,12 +337,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     const int32_t my_tile = lane / boxes, my_row = (lane % boxes) * box;
     constexpr int32_t kStep = C::PRODUCERS;
     // Window: lane k holds pair window + k, whose tiles are [w_end - w.g.n, w_end) of this CTA's run.
-    int32_t window = 0, w_end = 0;
+    int32_t window = sm.pair0 - 32, w_end = -sm.tile0;  // the pairs before the run: to be followed by its first 32
     DecodePair w = {};
-    auto load_window = [&](int32_t u0, int32_t at, bool cached) {  // `at`: where pair u0's tile 0 lies in the run
+    auto load_window = [&](int32_t u0, int32_t at) {  // `at`: where pair u0's tile 0 lies in the run
       window = u0;
       w = DecodePair{};
-      if (u0 + lane < pairs) w = cached ? sm.window[lane] : decode_pair(p, u0 + lane);
+      if (u0 + lane < pairs) {
+        if (per == 1 && u0 == sm.pair0) w = sm.window[lane];
+        else w = decode_pair(p, u0 + lane);
+      }
       w_end = w.g.n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -362,12 +364,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       nxt.need = false;
       if (i0 >= tiles) return 0;
       int32_t stop = __shfl_sync(0xffffffffu, w_end, 31);
+#pragma unroll 1
       while (stop <= i0) {
         if (window + 32 >= pairs) {  // only if the lengths changed while this call runs
           sm.abort = 1;
           return 0;
         }
-        load_window(window + 32, stop, false);
+        load_window(window + 32, stop);
         stop = __shfl_sync(0xffffffffu, w_end, 31);
       }
       stop = min(stop, tiles);
@@ -415,17 +418,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       }
       return min(batch_tiles, (stop - i0 + kStep - 1) / kStep);
     };
-    if (tiles > 0) {
-      load_window(sm.pair0, -sm.tile0, per == 1);
-      int32_t i = warp - C::WARPS, count = plan(i), issued = -1;  // issued: the last tile
+    {
+      int32_t i = warp - C::WARPS, count = 0, issued = -1;  // issued: the last tile
       bool ok = true;
-      while (count > 0 && ok) {
-        cur = nxt;
+      cur.need = false;
+#pragma unroll 1
+      for (;;) {
         const int32_t next_count = plan(i + count * kStep);
         if (cur.need && (uint32_t)cur.id >= (uint32_t)p.num_pages) {
           report(p.status, 1);
           cur.id = 0;
         }
+#pragma unroll 1
         for (int32_t j = 0; j < count; ++j, i += kStep) {
           const int s = i % C::STAGES;
           uint8_t* stage = ring + s * C::STAGE_BYTES;
@@ -467,10 +471,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           }
           __syncwarp();
         }
+        if (next_count == 0 || !ok) break;
         count = next_count;
+        cur = nxt;
       }
       // after a timeout: the copies in flight land before the block's memory is given up
       if (sm.abort)
+#pragma unroll 1
         for (int32_t k = issued; k >= 0 && k > issued - C::STAGES; k -= kStep)
           ptx::mbar_wait(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
     }
@@ -506,6 +513,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sm.sync);
       const uint32_t parity = meets++ & 1;
+#pragma unroll 1
       for (int spin = 0; spin < 256; ++spin)
         if (__all_sync(0xffffffffu, ptx::mbar_test_wait(&sm.sync, parity))) return true;
       ok = warp_wait(&sm.sync, parity, &sm.abort, p.status);
