@@ -39,7 +39,9 @@ namespace segpaged {
 
 constexpr int kDecodeTile = 128;         // tokens of a tile
 constexpr int kDecodeMaxWarps = 12;      // most consumer warps
-constexpr int kDecodeMaxProducers = 2;   // producer warps
+constexpr int kDecodeProducers = 2;      // helper warps that issue copies
+constexpr int kDecodeHelpers = 4;        // warps beside the consumers: one for each quarter of tensor memory's lanes
+constexpr int kDecodeMails = 2;          // finished chunks that tensor memory holds
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
 constexpr float kDecodeMinScale = 0x1p-120f;  // in place of a logit scale of 0: 0 x -infinity is not wanted
@@ -82,19 +84,28 @@ struct DecodeCfg {
   static constexpr int Q_BYTES = NB * 8 * D * 2;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int EXTRA_BYTES = SCALE_BYTES + Q_BYTES;      // beside a stage: exponent bytes, query rows
-  static constexpr int FIXED_BYTES = 4096 + 1024;                // barriers and small arrays, alignment slack
+  static constexpr int MERGE_BYTES = kDecodeHelpers * 8 * D * 4;  // a helper's sum of one column block of O
+  static constexpr int FIXED_BYTES = MERGE_BYTES + 4608 + 1024;  // + barriers and small arrays, alignment slack
   static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
   // A producer's wait for a stage looks at one parity bit, so the stage may be at most one use behind it: what it waited
-  // for before its last tile, PRODUCERS tiles ago, has to cover the use before the last one, 2 STAGES tiles ago.
-  static constexpr int PRODUCERS = STAGES < kDecodeMaxProducers ? STAGES : kDecodeMaxProducers;
-  static constexpr int THREADS = 32 * (WARPS + PRODUCERS);
-  static_assert(STAGES >= 2 && STAGES <= 8 && PRODUCERS <= STAGES, "ring");
-  static_assert(STAGE_BYTES >= 8 * 8 * D * 4, "a stage holds eight warps' O of one column block");
-  // What ending a pair costs a CTA, in half tiles: about 2.5 us. Of 5, 7, 9 and 12 for 8-bit pools of 128 columns 9
-  // measured best on 32 sequences of 16-32K (66.8, 65.6, 65.0, 66.5 us), 2, 3 and 4 for bf16 alike (106.1 to 105.8).
-  static constexpr int PAIR_COST = (FMT == kFmtBf16 ? 4 : 8) * 128 / D;
+  // for before its last tile, as many tiles ago as there are producers, has to cover the use before the last one,
+  // 2 STAGES tiles ago.
+  static_assert(STAGES >= 2 && STAGES <= 8 && kDecodeProducers <= STAGES, "ring");
+  static constexpr int THREADS = 32 * (WARPS + kDecodeHelpers);
+  // Tensor-memory columns of one warp's O in its quarter of the lanes, of a chunk, and of all of them.
+  static constexpr int OCOLS = NB * D / 4;
+  static constexpr int MAIL_COLS = (WARPS + 3) / 4 * OCOLS;
+  static constexpr int TMEM_COLS = kDecodeMails * MAIL_COLS <= 64 ? 64 : kDecodeMails * MAIL_COLS <= 128 ? 128 : 256;
+  static_assert(kDecodeMails * MAIL_COLS <= TMEM_COLS, "tensor memory");
+  static_assert(WARPS * 8 * NB <= 128 && WARPS % 4 == 0 && WARPS <= kDecodeMaxWarps, "a mail's arrays, the quarters");
+  // What ending a pair costs a CTA, in half tiles.
+#ifndef PC8
+#define PC8 3
+#define PC16 1
+#endif
+  static constexpr int PAIR_COST = (FMT == kFmtBf16 ? PC16 : PC8) * 128 / D;
 };
 
 template <bool B>
@@ -194,6 +205,32 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, status, kDecodeStatusTimeout));
 }
 
+// N (16 or 32) consecutive tensor-memory columns of this warp's lanes, to and from registers.
+template <int N>
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t* r) {
+  if constexpr (N == 32) {
+    ptx::tmem_st32(taddr, r);
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 32) {
+    ptx::tmem_ld32(taddr, r);
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  }
+}
+
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(dst)),
                "l"((uint64_t)__cvta_generic_to_global(src))
@@ -204,19 +241,28 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(ptx::smem_addr(bar)) : "memory");
 }
 
-// Shared memory beside the ring (4096 bytes).
+// A finished chunk as the consumers leave it for the helpers: each warp's maxima (log2 units), sums and unit of O, which
+// lies in tensor memory.
+struct DecodeMail {
+  float m[128], l[128], unit[kDecodeMaxWarps];  // [consumer warp][8 NB heads]: 12 x 8 or 8 x 16 of them
+  int32_t b, h0, slot, final;  // first sequence and head, partial slot or -1, whether it is the run's last chunk
+};
+
+// Shared memory beside the ring and the helpers' sums.
 struct DecodeSmall {
   uint64_t full[8], empty[8];
-  uint64_t sync;                                // consumers' meeting point
+  uint64_t mail_full[kDecodeMails], mail_empty[kDecodeMails];
+  uint64_t sync;                                // the helpers' meeting point
   DecodeTileHeader hdr[8];
-  float m[kDecodeMaxWarps][16], l[kDecodeMaxWarps][16];
-  int32_t warp_sum[kDecodeMaxWarps + kDecodeMaxProducers];
+  DecodeMail mail[kDecodeMails];
+  int32_t warp_sum[kDecodeMaxWarps + kDecodeHelpers];
   int32_t first_rank, end_rank;                 // this CTA's run in the list of all tiles
   int32_t pair0, tile0;                         // where its first tile lies
   int32_t abort;
+  uint32_t tmem;
   DecodePair window[32];                        // pairs pair0 ..
 };
-static_assert(sizeof(DecodeSmall) <= 4096, "small shared arrays");
+static_assert(sizeof(DecodeSmall) <= 4608, "small shared arrays");
 
 template <int D, int FMT, int NB>
 __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
@@ -226,7 +272,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* extras = ring + C::STAGES * C::STAGE_BYTES;
-  DecodeSmall& sm = *reinterpret_cast<DecodeSmall*>(extras + C::STAGES * C::EXTRA_BYTES);
+  float4* merge = reinterpret_cast<float4*>(extras + C::STAGES * C::EXTRA_BYTES);  // [helper][KS][lane]
+  DecodeSmall& sm = *reinterpret_cast<DecodeSmall*>(extras + C::STAGES * C::EXTRA_BYTES + C::MERGE_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t cta = blockIdx.x;
   const int32_t pairs = (p.B * p.Hkv) << p.log2_hg;
@@ -236,13 +283,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       ptx::mbar_init(&sm.full[s], BF ? 1 : 33);  // the copies' bytes; for 8-bit pools also each lane's cp.async
       ptx::mbar_init(&sm.empty[s], C::WARPS);
     }
-    ptx::mbar_init(&sm.sync, C::WARPS);
+    for (int k = 0; k < kDecodeMails; ++k) {
+      ptx::mbar_init(&sm.mail_full[k], C::WARPS);
+      ptx::mbar_init(&sm.mail_empty[k], kDecodeHelpers);
+    }
+    ptx::mbar_init(&sm.sync, kDecodeHelpers);
     ptx::mbar_fence_init();
     sm.abort = 0;
     sm.first_rank = sm.end_rank = 0;
     sm.pair0 = sm.tile0 = 0;
     ptx::tma_prefetch_desc(&tk);
     ptx::tma_prefetch_desc(&tv);
+  }
+  if (warp == C::WARPS) {
+    ptx::tmem_alloc(&sm.tmem, C::TMEM_COLS);
+    ptx::tmem_relinquish();
   }
   // The launch may start while the one before it ends; nothing it wrote is read, and nothing written, before this.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -267,10 +322,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     if (lane >= d) incl += x;
   }
   if (lane == 31) sm.warp_sum[warp] = incl;
+  ptx::tc_fence_before();
   __syncthreads();
+  ptx::tc_fence_after();
   int32_t before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < C::WARPS + C::PRODUCERS; ++w) {
+  for (int w = 0; w < C::WARPS + kDecodeHelpers; ++w) {
     const int32_t x = sm.warp_sum[w];
     if (w < warp) before += x;
     total += x;
@@ -317,6 +374,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   }
   __syncthreads();
   const int32_t first_rank = sm.first_rank, tiles = max(sm.end_rank - first_rank, 0);
+  const uint32_t tmem = sm.tmem + ((uint32_t)(warp & 3) << 21);  // this warp's quarter of the lanes
   if (per == 1) {
     const int32_t k = (int32_t)threadIdx.x - sm.pair0;
     if (k >= 0 && k < 32) sm.window[k] = own;
@@ -335,7 +393,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     const int32_t log2_box = min(p.log2_page, 6), box = 1 << log2_box;  // rows of one TMA box
     const int32_t boxes = kDecodeTile >> log2_box, batch_tiles = 32 / boxes;
     const int32_t my_tile = lane / boxes, my_row = (lane % boxes) * box;
-    constexpr int32_t kStep = C::PRODUCERS;
+    constexpr int32_t kStep = kDecodeProducers;
     // Window: lane k holds pair window + k, whose tiles are [w_end - w.g.n, w_end) of this CTA's run.
     int32_t window = sm.pair0 - 32, w_end = -sm.tile0;  // the pairs before the run: to be followed by its first 32
     DecodePair w = {};
@@ -418,35 +476,156 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       }
       return min(batch_tiles, (stop - i0 + kStep - 1) / kStep);
     };
-    {
-      int32_t i = warp - C::WARPS, count = 0, issued = -1;  // issued: the last tile
-      bool ok = true;
-      cur.need = false;
+    // Joins the warps' results of the chunk in mail `k`: each helper those of its quarter's warps (w, w + 4, w + 8), then
+    // all four together, a quarter of the columns each.
+    uint32_t meets = 0;
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.sync);
+      const uint32_t parity = meets++ & 1;
 #pragma unroll 1
-      for (;;) {
-        const int32_t next_count = plan(i + count * kStep);
+      for (int spin = 0; spin < 256; ++spin)
+        if (__all_sync(0xffffffffu, ptx::mbar_test_wait(&sm.sync, parity))) return true;
+      return warp_wait(&sm.sync, parity, &sm.abort, p.status);
+    };
+    constexpr int KS = D / 16, OC = D / 4;
+    const int g = lane >> 2, t = lane & 3, quarter = warp & 3;
+    auto join = [&](int k) {
+      const DecodeMail& mail = sm.mail[k];
+      ptx::tc_fence_after();
+      const int32_t b = mail.b, h0 = mail.h0, slot = mail.slot;
+#pragma unroll 1
+      for (int nb = 0; nb < NB; ++nb) {
+        const bool live = nb * 8 + 2 * t < heads;  // this lane's columns are heads of the group
+        // the largest m of this lane's two heads and the sum of all l to it: lane (g, t) looks at warps g and g + 8
+        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        float2 mx[2], lx[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mx[x] = make_float2(-INFINITY, -INFINITY);
+          lx[x] = make_float2(0.f, 0.f);
+          if (8 * x + g < C::WARPS) {
+            mx[x] = *reinterpret_cast<const float2*>(&mail.m[(8 * x + g) * 8 * NB + nb * 8 + 2 * t]);
+            lx[x] = *reinterpret_cast<const float2*>(&mail.l[(8 * x + g) * 8 * NB + nb * 8 + 2 * t]);
+          }
+          top[0] = fmaxf(top[0], mx[x].x);
+          top[1] = fmaxf(top[1], mx[x].y);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], d));
+          top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], d));
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          sum[0] += (mx[x].x == -INFINITY ? 0.f : ptx::ex2(mx[x].x - top[0])) * lx[x].x;
+          sum[1] += (mx[x].y == -INFINITY ? 0.f : ptx::ex2(mx[x].y - top[1])) * lx[x].y;
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
+          sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], d);
+        }
+        float acc[OC];
+#pragma unroll
+        for (int c = 0; c < OC; ++c) acc[c] = 0.f;
+#pragma unroll 1
+        for (int x = 0; x < C::WARPS / 4; ++x) {
+          uint32_t r[OC];
+          tmem_get<OC>(tmem + k * C::MAIL_COLS + x * C::OCOLS + nb * OC, r);
+          const int from = quarter + 4 * x;  // consumer warp w is on the quarter w mod 4
+          const float2 mw = *reinterpret_cast<const float2*>(&mail.m[from * 8 * NB + nb * 8 + 2 * t]);
+          const float unit = BF ? 1.f : mail.unit[from];
+          const float w0 = mw.x == -INFINITY ? 0.f : ptx::ex2(mw.x - top[0]) * unit;
+          const float w1 = mw.y == -INFINITY ? 0.f : ptx::ex2(mw.y - top[1]) * unit;
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < OC; ++c) acc[c] += __uint_as_float(r[c]) * (c & 1 ? w1 : w0);
+        }
+        float4* mine = merge + quarter * KS * 32 + lane;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt)
+          mine[mt * 32] = make_float4(acc[4 * mt], acc[4 * mt + 1], acc[4 * mt + 2], acc[4 * mt + 3]);
+        if (!meet()) return false;
+        if (live) {
+          const float inv[2] = {__fdividef(1.f, sum[0]), __fdividef(1.f, sum[1])};
+#pragma unroll
+          for (int y = 0; y < KS / 4; ++y) {
+            const int mt = quarter * (KS / 4) + y;
+            float4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = merge[(x * KS + mt) * 32 + lane];
+            const float out[2][2] = {{(v[0].x + v[1].x) + (v[2].x + v[3].x), (v[0].z + v[1].z) + (v[2].z + v[3].z)},
+                                     {(v[0].y + v[1].y) + (v[2].y + v[3].y), (v[0].w + v[1].w) + (v[2].w + v[3].w)}};
+            const int d0 = 16 * mt + (BF ? g : 2 * g), d1 = d0 + (BF ? 8 : 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // out[head][dim]
+              const int head = nb * 8 + 2 * t + j;
+              if (head >= heads) continue;
+              if (slot < 0) {
+                __nv_bfloat16* to = p.o + ((int64_t)b * Hq + h0 + head) * D;
+                to[d0] = __float2bfloat16_rn(out[j][0] * inv[j]);
+                to[d1] = __float2bfloat16_rn(out[j][1] * inv[j]);
+              } else {
+                float* to = p.part_o + ((int64_t)slot * kDecodeGroup + head) * D;
+                to[d0] = out[j][0] * inv[j];
+                to[d1] = out[j][1] * inv[j];
+              }
+            }
+          }
+          if (quarter == 0 && g == 0)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int head = nb * 8 + 2 * t + j;
+              if (head >= heads) continue;
+              const float lse2 = top[j] + log2f(sum[j]);
+              if (slot < 0) p.lse[(int64_t)(h0 + head) * p.B + b] = 0.6931471805599453f * lse2;
+              else p.part_lse[(int64_t)slot * kDecodeGroup + head] = lse2;
+            }
+        }
+        if (!meet()) return false;  // `merge` is free again
+      }
+      ptx::tc_fence_before();
+      return true;
+    };
+
+    // Both jobs in turn: a copy as soon as its stage is free, a join as soon as a chunk is in the mail.
+    int32_t i = warp - C::WARPS, left = 0, at_box = 0, ahead = -1, issued = -1;  // issued: the last tile
+    bool producing = tiles > 0 && i < kStep, done = tiles == 0;
+    uint32_t mails = 0;
+    int32_t idle = 0;
+    cur.need = nxt.need = false;
+#pragma unroll 1
+    while (producing || !done) {
+      if (producing && left == 0) {  // the batch that was planned last becomes the current one
+        if (ahead == 0) {
+          producing = false;
+          continue;
+        }
+        cur = nxt;
+        left = max(ahead, 0);
+        at_box = 0;
+        ahead = plan(i + left * kStep);
         if (cur.need && (uint32_t)cur.id >= (uint32_t)p.num_pages) {
           report(p.status, 1);
           cur.id = 0;
         }
-#pragma unroll 1
-        for (int32_t j = 0; j < count; ++j, i += kStep) {
-          const int s = i % C::STAGES;
+        continue;
+      }
+      if (producing) {
+        const int s = i % C::STAGES;
+        if (i < C::STAGES || __all_sync(0xffffffffu, ptx::mbar_try_wait(&sm.empty[s], ((i / C::STAGES) - 1) & 1))) {
+          idle = 0;
           uint8_t* stage = ring + s * C::STAGE_BYTES;
           uint8_t* extra = extras + s * C::EXTRA_BYTES;
-          if (i >= C::STAGES && !warp_wait(&sm.empty[s], ((i / C::STAGES) - 1) & 1, &sm.abort, p.status)) {
-            ok = false;
-            break;
-          }
-          const bool load = my_tile == j && cur.need;
+          const bool load = my_tile == at_box && cur.need;
           const uint32_t have = __ballot_sync(0xffffffffu, load);
-          if (lane == j * boxes) {
+          if (lane == at_box * boxes) {
             const bool with_q = cur.h.flags & 1;
             sm.hdr[s] = cur.h;
             ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + (with_q ? heads * D * 2 : 0));
-            if (with_q) {
+            if (with_q)
               bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)cur.h.b * Hq + cur.h.h0) * D, heads * D * 2, &sm.full[s]);
-            }
           }
           issued = i;
           __syncwarp();
@@ -461,7 +640,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           if (!BF) {
             // The tile's exponent bytes, [page][K, V][row], 16 of them a lane: a bulk copy per page would be as many
             // copies again as the codes take where pages are small.
-            const int32_t at = lane * 16, from = j * boxes + ((at >> (p.log2_page + 1)) << p.log2_page >> log2_box);
+            const int32_t at = lane * 16, from = at_box * boxes + ((at >> (p.log2_page + 1)) << p.log2_page >> log2_box);
             // of a page of two boxes, either may be the only one that is loaded
             const int32_t box_at = (p.log2_page == log2_box || (have >> (from & 31) & 1) ? from : from + 1) & 31;
             const int32_t id = __shfl_sync(0xffffffffu, cur.id, box_at);
@@ -470,17 +649,37 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             cp_async_arrive(&sm.full[s]);
           }
           __syncwarp();
+          --left;
+          ++at_box;
+          i += kStep;
         }
-        if (next_count == 0 || !ok) break;
-        count = next_count;
-        cur = nxt;
       }
-      // after a timeout: the copies in flight land before the block's memory is given up
-      if (sm.abort)
-#pragma unroll 1
-        for (int32_t k = issued; k >= 0 && k > issued - C::STAGES; k -= kStep)
-          ptx::mbar_wait(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
+      if (!done) {
+        const int k = mails % kDecodeMails;
+        const uint32_t parity = mails / kDecodeMails & 1;
+        if (__all_sync(0xffffffffu, producing ? ptx::mbar_test_wait(&sm.mail_full[k], parity)
+                                              : ptx::mbar_try_wait(&sm.mail_full[k], parity))) {
+          idle = 0;
+          done = sm.mail[k].final != 0;
+          if (!join(k)) break;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.mail_empty[k]);
+          ++mails;
+        }
+      }
+      if ((++idle & 63) == 0) {  // a bounded wait, as ptx::mbar_wait: seconds of tries of 200 ns
+        if (idle > 1 << 24) {
+          sm.abort = 1;
+          report(p.status, kDecodeStatusTimeout);
+        }
+        if (__any_sync(0xffffffffu, *(volatile int32_t*)&sm.abort != 0)) break;
+      }
     }
+    // after a timeout: the copies in flight land before the block's memory is given up
+    if (*(volatile int32_t*)&sm.abort)
+#pragma unroll 1
+      for (int32_t k = issued; k >= 0 && k > issued - C::STAGES; k -= kStep)
+        ptx::mbar_wait(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
   } else {
     // ----------------------------------------------------------------------------------- consumers
     constexpr int KS = D / 16;  // k16 steps of a logit, and m16 tiles of O^T
@@ -507,21 +706,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     float head_scale[NB][2];                     // of heads 2t, 2t + 1
     float m[NB][2], l[NB][2], o[NB][KS][4];
     int32_t vref = 0;                            // r + 127
-    uint32_t meets = 0;
-    bool ok = true;
-    auto meet = [&]() {                          // all consumer warps (bounded, unlike a block barrier)
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sm.sync);
-      const uint32_t parity = meets++ & 1;
-#pragma unroll 1
-      for (int spin = 0; spin < 256; ++spin)
-        if (__all_sync(0xffffffffu, ptx::mbar_test_wait(&sm.sync, parity))) return true;
-      ok = warp_wait(&sm.sync, parity, &sm.abort, p.status);
-      return ok;
-    };
+    uint32_t mails = 0;
     int tick = 0, s = -1;
     uint32_t phase = 1;
-    for (int32_t i = 0; i < tiles && ok; ++i) {
+    for (int32_t i = 0; i < tiles; ++i) {
       s = s + 1 == C::STAGES ? 0 : s + 1;
       phase ^= s == 0;
       if (!warp_wait(&sm.full[s], phase, &sm.abort, p.status)) break;
@@ -764,135 +952,51 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         if (row0 < v0 || row0 + 16 * MB > v1) process(Flag<true>{});
         else process(Flag<false>{});
       }
-      if (!(h.flags & 2)) {
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);  // this warp has read its rows
-        continue;
-      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);  // this warp has read its rows
+      if (!(h.flags & 2)) continue;
 
-      // ---- a chunk ends: the warps' results become one, through the stage of its last tile
-      const int32_t b = h.b, h0 = h.h0, slot = (h.flags >> 2) - 1;
+      // ---- a chunk ends: this warp's result goes into the mail, and it goes on to the next chunk
+      const int k = mails % kDecodeMails;
+      if (mails >= kDecodeMails && !warp_wait(&sm.mail_empty[k], (mails / kDecodeMails - 1) & 1, &sm.abort, p.status)) break;
+      ++mails;
+      ptx::tc_fence_after();
+      DecodeMail& mail = sm.mail[k];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
-          if (m[nb][j] != -INFINITY) m[nb][j] *= head_scale[nb][j];  // to log2 units
           if (g == 0) {
-            sm.m[warp][nb * 8 + 2 * t + j] = m[nb][j];
-            sm.l[warp][nb * 8 + 2 * t + j] = l[nb][j];
+            mail.m[(warp * NB + nb) * 8 + 2 * t + j] = m[nb][j] == -INFINITY ? m[nb][j] : m[nb][j] * head_scale[nb][j];
+            mail.l[(warp * NB + nb) * 8 + 2 * t + j] = l[nb][j];
           }
         }
-      if (!meet()) break;  // from here no warp reads the tile any more
-      float4* scratch = reinterpret_cast<float4*>(ring + s * C::STAGE_BYTES);  // [8][KS][lane]
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const bool live = nb * 8 + 2 * t < heads;  // this lane's columns are heads of the group
-        // the largest m of this lane's two heads and the sum of all l to it: lane (g, t) looks at warps g and g + 8
-        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, w[2];
-        float2 mx[2], lx[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          mx[x] = make_float2(-INFINITY, -INFINITY);
-          lx[x] = make_float2(0.f, 0.f);
-          if (8 * x + g < C::WARPS) {
-            mx[x] = *reinterpret_cast<const float2*>(&sm.m[8 * x + g][nb * 8 + 2 * t]);
-            lx[x] = *reinterpret_cast<const float2*>(&sm.l[8 * x + g][nb * 8 + 2 * t]);
-          }
-          top[0] = fmaxf(top[0], mx[x].x);
-          top[1] = fmaxf(top[1], mx[x].y);
-        }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], d));
-          top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], d));
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          sum[0] += (mx[x].x == -INFINITY ? 0.f : ptx::ex2(mx[x].x - top[0])) * lx[x].x;
-          sum[1] += (mx[x].y == -INFINITY ? 0.f : ptx::ex2(mx[x].y - top[1])) * lx[x].y;
-        }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], d);
-          sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], d);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          w[j] = m[nb][j] == -INFINITY ? 0.f : ptx::ex2(m[nb][j] - top[j]);
-          if (!BF) w[j] *= exp2_int(vref - 127 - 14);
-        }
-        float4* mine_o = scratch + (warp & 7) * KS * 32 + lane;
-        float4 scaled[KS];
-#pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
-          scaled[mt] = make_float4(o[nb][mt][0] * w[0], o[nb][mt][1] * w[1], o[nb][mt][2] * w[0], o[nb][mt][3] * w[1]);
-        if (C::WARPS > 8) {  // the scratch has room for eight: the others' go to their partners first
-          if (warp >= 8 && live)
-#pragma unroll
-            for (int mt = 0; mt < KS; ++mt) mine_o[mt * 32] = scaled[mt];
-          if (!meet()) break;
-          if (warp < C::WARPS - 8 && live)
-#pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-              const float4 v = mine_o[mt * 32];
-              scaled[mt].x += v.x;
-              scaled[mt].y += v.y;
-              scaled[mt].z += v.z;
-              scaled[mt].w += v.w;
-            }
-        }
-        if (warp < 8 && live)
-#pragma unroll
-          for (int mt = 0; mt < KS; ++mt) mine_o[mt * 32] = scaled[mt];
-        if (!meet()) break;
-        // warp x finishes the 16 dims of m-tile x; this lane's heads are again 2t, 2t + 1
-        if (warp < KS && live) {
-          const float4* from = scratch + warp * 32 + lane;
-          float4 v[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = from[x * KS * 32];
-#pragma unroll
-          for (int d = 4; d > 0; d >>= 1)
-#pragma unroll
-            for (int x = 0; x < d; ++x) {
-              v[x].x += v[x + d].x;
-              v[x].y += v[x + d].y;
-              v[x].z += v[x + d].z;
-              v[x].w += v[x + d].w;
-            }
-          const float out[2][2] = {{v[0].x, v[0].z}, {v[0].y, v[0].w}};  // [head][dim]
-          const int d0 = 16 * warp + (BF ? g : 2 * g), d1 = d0 + (BF ? 8 : 1);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int head = nb * 8 + 2 * t + j;
-            if (head >= heads) continue;
-            const float inv = __fdividef(1.f, sum[j]);
-            if (slot < 0) {
-              __nv_bfloat16* to = p.o + ((int64_t)b * Hq + h0 + head) * D;
-              to[d0] = __float2bfloat16_rn(out[j][0] * inv);
-              to[d1] = __float2bfloat16_rn(out[j][1] * inv);
-            } else {
-              float* to = p.part_o + ((int64_t)slot * kDecodeGroup + head) * D;
-              to[d0] = out[j][0] * inv;
-              to[d1] = out[j][1] * inv;
-            }
-            if (warp == 0 && g == 0) {
-              const float lse2 = top[j] + log2f(sum[j]);
-              if (slot < 0) p.lse[(int64_t)(h0 + head) * p.B + b] = 0.6931471805599453f * lse2;
-              else p.part_lse[(int64_t)slot * kDecodeGroup + head] = lse2;
-            }
-          }
-        }
-        if (nb + 1 < NB && !meet()) break;  // the scratch is free again
+        tmem_put<D / 4>(tmem + k * C::MAIL_COLS + (warp >> 2) * C::OCOLS + nb * (D / 4),
+                        reinterpret_cast<const uint32_t*>(&o[nb][0][0]));
       }
-      ptx::fence_proxy_async_smem();  // the scratch was written by plain stores; the next writer is a TMA copy
+      if (lane == 0) {
+        mail.unit[warp] = BF ? 1.f : exp2_int(vref - 127 - 14);
+        if (warp == 0) {
+          mail.b = h.b;
+          mail.h0 = h.h0;
+          mail.slot = (h.flags >> 2) - 1;
+          mail.final = i + 1 == tiles;
+        }
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sm.empty[s]);
+      if (lane == 0) ptx::mbar_arrive(&sm.mail_full[k]);
     }
   }
+  ptx::tc_fence_before();
   __syncthreads();
+  if (warp == C::WARPS) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(sm.tmem, C::TMEM_COLS);
+  }
 }
 
 // Joins the chunks of the pairs that several CTAs shared: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
