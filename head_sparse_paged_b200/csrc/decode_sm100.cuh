@@ -69,9 +69,11 @@ struct DecodeParams {
 
 template <int D, int FMT, int NB>
 struct DecodeCfg {
-  // A warp takes 32 tokens of every second tile: two independent chains of products, and one maximum, wait and header
-  // for twice the tokens. With 16 heads the registers allow 16 tokens of every tile.
-  static constexpr int MB = NB == 1 ? 2 : 1;
+  // A warp takes 32 tokens of every second or third tile: two independent chains of products, and one maximum, wait and
+  // header for twice the tokens. (16 tokens of every tile: 89.2 instead of 80.5 us with 16 heads on 32 sequences of
+  // 16-32K in e4m3.) Twelve consumer warps leave 128 registers a thread, too few for the O and q of 16 heads; for bf16
+  // pools, whose stages are three, a third turn would only hold one more of them (see STAGES).
+  static constexpr int MB = 2;
   static constexpr int WARPS = NB == 1 && FMT != kFmtBf16 ? 12 : 8;               // consumer warps
   static constexpr int TILE_WARPS = kDecodeTile / (16 * MB);     // of which these share a tile
   static constexpr int TURNS = WARPS / TILE_WARPS;
@@ -100,12 +102,10 @@ struct DecodeCfg {
   static constexpr int TMEM_COLS = kDecodeMails * MAIL_COLS <= 64 ? 64 : kDecodeMails * MAIL_COLS <= 128 ? 128 : 256;
   static_assert(kDecodeMails * MAIL_COLS <= TMEM_COLS, "tensor memory");
   static_assert(WARPS * 8 * NB <= 128 && WARPS % 4 == 0 && WARPS <= kDecodeMaxWarps, "a mail's arrays, the quarters");
-  // What ending a pair costs a CTA, in half tiles.
-#ifndef PC8
-#define PC8 3
-#define PC16 1
-#endif
-  static constexpr int PAIR_COST = (FMT == kFmtBf16 ? PC16 : PC8) * 128 / D;
+  // What ending a pair costs a CTA, in half tiles of 128 columns. Of 3, 5, 7 and 9 for 8-bit pools 32 sequences of 16-32K
+  // took 65.3, 63.4, 62.8 and 62.9 us and 64 of 0.1-0.9K 23.9, 22.8, 22.9 and 23.1 us; of 1, 2, 4 and 6 for bf16 108.8,
+  // 107.0, 106.9, 107.4 us and 30.5, 25.6, 24.5, 24.7 us.
+  static constexpr int PAIR_COST = FMT == kFmtBf16 ? 3 : 6;
 };
 
 template <bool B>
