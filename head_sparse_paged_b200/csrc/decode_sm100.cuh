@@ -3,28 +3,39 @@
 // For sequence b, KV head k and the G query heads h of its group, at position i = L - 1:
 //   s_j = scale q_h . k_j over the visible keys j,  O_h = sum_j softmax(s)_j v_j,  LSE_h = ln sum_j exp(s_j).
 // Every visible key and value is read once and used by G heads only, so the call is bound by HBM (for G = 8, 16
-// flops per bf16 byte; the tensor cores pass 60 flops per byte here even through mma.sync). What matters is that
-// all SMs load all the time. So:
+// flops per bf16 byte, where mma.sync passes about 60). What matters is that all SMs load all the time. So:
 //   - The work is the list of 128-token tiles of all (sequence, KV head) pairs, cut into one equal run of tiles per
-//     CTA (one persistent CTA per SM): a pair's tiles may end in one CTA and go on in the next. Each CTA finds its run
-//     by itself from ctx_len and the classes in device memory (a prefix sum over the pairs, 1-2 us), so a captured
-//     call follows the lengths and there is no host plan. Runs that end inside a pair leave a partial result
-//     (O / l and its log2-sum) in the workspace, which decode_combine_kernel joins in tile order: no atomics, and the
+//     CTA (one CTA per SM): a pair's tiles may end in one CTA and go on in the next. Each CTA finds its run by itself
+//     from ctx_len and the classes in device memory (a prefix sum over the pairs, 1.5 us), so a captured call follows the
+//     lengths and there is no host plan. Runs that end inside a pair leave a partial result (O / l and its log2-sum) in
+//     the workspace, which decode_combine_kernel joins in tile order: no atomics, no state from call to call, and the
 //     result depends on the lengths and the grid only.
-//   - A producer warp streams the tiles through a ring of shared-memory stages with TMA (page id = coordinate), up to
-//     three (bf16) or six (8-bit) 128-token tiles ahead, across pair boundaries, with the page ids of the next tile
-//     fetched while it waits for a free stage.
-//   - Eight consumer warps take 16 tokens of each tile, and keep their own running maximum, sum and O in registers;
-//     they meet only where a pair ends. S^T = K Q^T puts the tokens on the 16 rows of mma.m16n8k16 and the heads on
-//     its 8 columns, so up to 8 heads cost the same and nothing is padded from 8 to 16; O^T = V^T P^T likewise.
-//   - tcgen05 would need the tile's rows as its 128-row M and TMEM round trips for an S of 128 x 8; the work is a
-//     sixth of what mma.sync can do in the time the bytes take, so the legacy path is the shorter one here.
+//   - Two of four helper warps stream the tiles through a ring of shared-memory stages with TMA (page id = coordinate),
+//     three (bf16) or six (8-bit) tiles deep, across pair boundaries, with the page ids of the next tiles in flight.
+//   - Eight (bf16) or twelve (8-bit) consumer warps take 32 tokens of every second or third tile, and keep their own
+//     running maximum, sum and O in registers. S^T = K Q^T puts the tokens on the 16 rows of mma.m16n8k16 and the heads
+//     on its 8 columns, so up to 8 heads cost the same and nothing is padded from 8 to 16; O^T = V^T P^T likewise.
+//   - Where a pair ends, a consumer leaves its maxima and sums in shared memory and its O in tensor memory (0.25 us) and
+//     goes on; the four helpers, one to each quarter of tensor memory's lanes, join the warps' results. (When the
+//     consumers met and joined them themselves, all of them waited for the last one's tile and then for one another: 1.7 us
+//     per pair and CTA; 65.5 instead of 63.3 us on 32 sequences of 16-32K in e4m3, 71.0 instead of 65.9 us in int8, 27.5
+//     instead of 22.8 us on 64 sequences of 0.1-0.9K.)
+//   - tcgen05.mma would need the tile's rows as its 128-row M and TMEM round trips for an S of 128 x 8; the work is a
+//     fifth of what mma.sync can do in the time the bytes take, so the legacy path is the shorter one here.
 // 8-bit pools: codes become fp16 in registers (exact). Query rows are brought to a largest magnitude of 2^15 by a power
 // of two first, so that bf16 queries of any size are exact in fp16 to 2^-29 of the row's largest. The K row's exponent
 // scales the logit; the V row's exponent 2^(y - r), r the largest one so far in this warp, multiplies the
 // probability, and O is kept in units of 2^(r - 14): the product, at most 2^14, is rounded to fp16 (2^-11 relative
 // down to 2^-28 of the largest). bf16 pools: a probability is split into a sum of two bf16 (2^-16 relative), which
 // costs a second V product where the tensor pipe idles.
+//
+// Measured (B200, back-to-back calls; of the 6543 GB/s that a large copy reaches): 32 sequences of 16-32K, 64/8 heads,
+// one global head each: bf16 106.9 us, 6.1 TB/s (94 %); e4m3 63.3 us, 5.2 TB/s (80 %); int8 65.9 us. 64 global heads at
+// 128K: bf16 612 us, 7.0 TB/s (107 %); e4m3 322 us, 6.7 TB/s (103 %), 344 us after seconds of it, when the power cap
+// holds the SMs at 1.6 GHz and the conversions' ALU work (53 % of its pipe at 1.9 GHz) no longer hides. What the short
+// calls are made of, on 32 sequences in e4m3: 2.6 us to find the run, 2.3 us to the first copy, 2.3 us to the first tile, 47 us
+// of tiles, 2 us to the last chunk's results, 1.2 us to the combine kernel's start, 2.6 us in it, and 4 us between the
+// mean and the last CTA.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -244,7 +255,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // A finished chunk as the consumers leave it for the helpers: each warp's maxima (log2 units), sums and unit of O, which
 // lies in tensor memory.
 struct DecodeMail {
-  float m[128], l[128], unit[kDecodeMaxWarps];  // [consumer warp][8 NB heads]: 12 x 8 or 8 x 16 of them
+  float m[128], l[128];             // [consumer warp][8 NB heads]: 12 x 8 or 8 x 16 of them
+  int32_t vref[kDecodeMaxWarps];    // the exponent byte r + 127 of the unit 2^(r - 14) of its O
   int32_t b, h0, slot, final;  // first sequence and head, partial slot or -1, whether it is the run's last chunk
 };
 
@@ -494,6 +506,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       const DecodeMail& mail = sm.mail[k];
       ptx::tc_fence_after();
       const int32_t b = mail.b, h0 = mail.h0, slot = mail.slot;
+      // The largest unit of the warps' O. It is applied to the finished quotients: as part of a weight it would take
+      // values near the smallest floats below them.
+      const int32_t vtop = BF ? 0 : __reduce_max_sync(0xffffffffu, lane < C::WARPS ? mail.vref[lane] : 0);
+      const float unit = BF ? 1.f : row_scale(vtop);
 #pragma unroll 1
       for (int nb = 0; nb < NB; ++nb) {
         const bool live = nb * 8 + 2 * t < heads;  // this lane's columns are heads of the group
@@ -535,9 +551,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           tmem_get<OC>(tmem + k * C::MAIL_COLS + x * C::OCOLS + nb * OC, r);
           const int from = quarter + 4 * x;  // consumer warp w is on the quarter w mod 4
           const float2 mw = *reinterpret_cast<const float2*>(&mail.m[from * 8 * NB + nb * 8 + 2 * t]);
-          const float unit = BF ? 1.f : mail.unit[from];
-          const float w0 = mw.x == -INFINITY ? 0.f : ptx::ex2(mw.x - top[0]) * unit;
-          const float w1 = mw.y == -INFINITY ? 0.f : ptx::ex2(mw.y - top[1]) * unit;
+          const float rel = BF ? 1.f : exp2_int(mail.vref[from] - vtop - 14);
+          const float w0 = mw.x == -INFINITY ? 0.f : ptx::ex2(mw.x - top[0]) * rel;
+          const float w1 = mw.y == -INFINITY ? 0.f : ptx::ex2(mw.y - top[1]) * rel;
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < OC; ++c) acc[c] += __uint_as_float(r[c]) * (c & 1 ? w1 : w0);
@@ -564,12 +580,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
               if (head >= heads) continue;
               if (slot < 0) {
                 __nv_bfloat16* to = p.o + ((int64_t)b * Hq + h0 + head) * D;
-                to[d0] = __float2bfloat16_rn(out[j][0] * inv[j]);
-                to[d1] = __float2bfloat16_rn(out[j][1] * inv[j]);
+                to[d0] = __float2bfloat16_rn(out[j][0] * inv[j] * unit);
+                to[d1] = __float2bfloat16_rn(out[j][1] * inv[j] * unit);
               } else {
                 float* to = p.part_o + ((int64_t)slot * kDecodeGroup + head) * D;
-                to[d0] = out[j][0] * inv[j];
-                to[d1] = out[j][1] * inv[j];
+                to[d0] = out[j][0] * inv[j] * unit;
+                to[d1] = out[j][1] * inv[j] * unit;
               }
             }
           }
@@ -861,8 +877,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           n1 = fmaxf(n1, m[nb][1]);
           // a larger maximum (or V exponent) rescales what was summed so far
           if (__any_sync(0xffffffffu, n0 != m[nb][0] || n1 != m[nb][1] || vshift != 1.f)) {
-            const float c0 = m[nb][0] == -INFINITY ? 0.f : ptx::ex2(f0 * (m[nb][0] - n0));
-            const float c1 = m[nb][1] == -INFINITY ? 0.f : ptx::ex2(f1 * (m[nb][1] - n1));
+            // (the difference of the rounded f m that the probabilities are relative to, not f times the difference)
+            const float c0 = m[nb][0] == -INFINITY ? 0.f : ptx::ex2(__fmul_rn(f0, m[nb][0]) - __fmul_rn(f0, n0));
+            const float c1 = m[nb][1] == -INFINITY ? 0.f : ptx::ex2(__fmul_rn(f1, m[nb][1]) - __fmul_rn(f1, n1));
             // NaN sums stay NaN: 0 * NaN
             l[nb][0] *= c0;
             l[nb][1] *= c1;
@@ -877,7 +894,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             m[nb][0] = n0;
             m[nb][1] = n1;
           }
-          const float b0 = n0 == -INFINITY ? 0.f : -f0 * n0, b1 = n1 == -INFINITY ? 0.f : -f1 * n1;
+          const float b0 = n0 == -INFINITY ? 0.f : -__fmul_rn(f0, n0), b1 = n1 == -INFINITY ? 0.f : -__fmul_rn(f1, n1);
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -969,7 +986,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
           if (g == 0) {
-            mail.m[(warp * NB + nb) * 8 + 2 * t + j] = m[nb][j] == -INFINITY ? m[nb][j] : m[nb][j] * head_scale[nb][j];
+            mail.m[(warp * NB + nb) * 8 + 2 * t + j] = m[nb][j] == -INFINITY ? m[nb][j] : __fmul_rn(head_scale[nb][j], m[nb][j]);
             mail.l[(warp * NB + nb) * 8 + 2 * t + j] = l[nb][j];
           }
         }
@@ -977,7 +994,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
                         reinterpret_cast<const uint32_t*>(&o[nb][0][0]));
       }
       if (lane == 0) {
-        mail.unit[warp] = BF ? 1.f : exp2_int(vref - 127 - 14);
+        mail.vref[warp] = vref;
         if (warp == 0) {
           mail.b = h.b;
           mail.h0 = h.h0;

@@ -53,13 +53,14 @@ __device__ __forceinline__ HeadPages head_pages(const int32_t* ctx_len, const in
   return head_pages(ctx_len[b], max(q_len ? q_len[b] : 1, min_q), cls, bk, log2_page);
 }
 
-// Largest index i in [0, n) with start[i] <= x, for ascending starts and start[0] <= x: 32 of them a round.
+// Largest index i in [0, n) with start[i] <= x (0 if there is none), for ascending starts: 32 of them a round. Whatever
+// the array holds, the result is in [0, n).
 __device__ __forceinline__ int32_t warp_find(const int32_t* start, int32_t n, int64_t x) {
   int32_t lo = 0;
   while (n > 1) {
     const int32_t step = (n + 31) >> 5, i = (threadIdx.x & 31) * step;
     const bool le = i < n && start[lo + i] <= x;
-    const int32_t k = (__popc(__ballot_sync(0xffffffffu, le)) - 1) * step;
+    const int32_t k = max(__popc(__ballot_sync(0xffffffffu, le)) - 1, 0) * step;
     lo += k;
     n = min(step, n - k);
   }
@@ -108,21 +109,22 @@ __global__ void __launch_bounds__(32 * kSliceWarps) build_quant_kernel(BuildQuan
   constexpr int LANES = D / 16, ROWS = 32 / LANES, N = kSliceRows / ROWS;  // lanes of a row, rows a pass, passes
   const int lane = threadIdx.x & 31, c = lane % LANES;
   const int nheads = p.B * p.Hkv, log2_slices = q.log2_page - kLog2SliceRows;
-  const int64_t slices = q.table_len << log2_slices, entries = p.offs[nheads];
+  const int64_t slices = q.table_len << log2_slices, begin = p.offs[0], entries = p.offs[nheads];
   if (blockIdx.x == 0 && threadIdx.x == 0 && entries > q.table_len) report(p.status, 2);
   const int64_t warps = (int64_t)gridDim.x * kSliceWarps;
   for (int64_t x = (int64_t)blockIdx.x * kSliceWarps + (threadIdx.x >> 5); x < slices; x += warps) {
     const int64_t e = x >> log2_slices;
     const int32_t row0 = (int32_t)(x & ((1 << log2_slices) - 1)) * kSliceRows;
     const int32_t pid = p.table[e];
-    if (e >= entries) break;  // spare room behind the last table
+    if (e < begin) continue;  // spare room before the first table
+    if (e >= entries) break;  // and behind the last
     const int bk = warp_find(p.offs, nheads, e), b = bk / p.Hkv, kh = bk - b * p.Hkv;
     const int32_t t = (int32_t)(e - p.offs[bk]);
     const int64_t src0 = p.cu_k[b];
     const HeadPages hp = head_pages((int32_t)(p.cu_k[b + 1] - src0), max(p.q_len[b], 0), p.cls, bk, q.log2_page);
     if (p.offs[bk + 1] - p.offs[bk] != hp.total) {
-      if (t == 0 && lane == 0) report(p.status, 2);
-      if (t >= hp.total) continue;
+      if (lane == 0) report(p.status, 2);
+      if (t < 0 || t >= hp.total) continue;
     }
     if (pid < 0 || pid >= p.num_pages) {
       if (lane == 0) report(p.status, 1);
@@ -286,14 +288,15 @@ __global__ void __launch_bounds__(32 * kSliceWarps) dequant_pages_kernel(Dequant
   constexpr int LANES = D / 8, ROWS = 32 / LANES, N = kSliceRows / ROWS;
   const int lane = threadIdx.x & 31, c = lane % LANES;
   const int nheads = p.B * p.Hkv, log2_slices = p.log2_page - kLog2SliceRows;
-  const int64_t slices = p.table_len << log2_slices, entries = p.offs[nheads];
+  const int64_t slices = p.table_len << log2_slices, begin = p.offs[0], entries = p.offs[nheads];
   const int64_t warps = (int64_t)gridDim.x * kSliceWarps;
   if (blockIdx.x == 0 && threadIdx.x == 0 && entries > p.table_len) report(p.status, 2);
   for (int64_t x = (int64_t)blockIdx.x * kSliceWarps + (threadIdx.x >> 5); x < slices; x += warps) {
     const int64_t e = x >> log2_slices;
     const int32_t row0 = (int32_t)(x & ((1 << log2_slices) - 1)) * kSliceRows;
     const int32_t pid = p.table[e];
-    if (e >= entries) break;  // spare room behind the last table
+    if (e < begin) continue;  // spare room before the first table
+    if (e >= entries) break;  // and behind the last
     if (pid < 0 || pid >= p.num_pages) {
       if (lane == 0) report(p.status, 1);
       continue;
@@ -314,8 +317,8 @@ __global__ void __launch_bounds__(32 * kSliceWarps) dequant_pages_kernel(Dequant
     const int32_t t = (int32_t)(e - p.offs[bk]);
     const HeadPages hp = head_pages(p.ctx_len, p.q_len, p.cls, b, bk, p.log2_page, 0);
     if (p.offs[bk + 1] - p.offs[bk] != hp.total) {
-      if (t == 0 && lane == 0) report(p.status, 2);
-      if (t >= hp.total) continue;
+      if (lane == 0) report(p.status, 2);
+      if (t < 0 || t >= hp.total) continue;
     }
     const int64_t tok0 = ((int64_t)hp.logical(t) << p.log2_page) + row0 + lane / LANES;
 #pragma unroll

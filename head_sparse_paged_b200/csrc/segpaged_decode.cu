@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/segpaged.h"
@@ -282,6 +283,7 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   if (!q || (!page_table && page_table_len > 0) || !page_table_offs || !ctx_len || !cls || !o || !lse || !workspace) return SEGPAGED_ERR_NULL;
   if (workspace_bytes < segpaged_decode_workspace_bytes(dims)) return SEGPAGED_ERR_CAPACITY;
   if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return SEGPAGED_ERR_ALIGN;
+  if (!std::isfinite(softmax_scale)) return SEGPAGED_ERR_DIMS;
   const int sms = sm_count();
   if (sms <= 0) return SEGPAGED_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

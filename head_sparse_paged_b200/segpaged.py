@@ -164,10 +164,10 @@ def _dev(t: torch.Tensor | None, dtype=None, what=""):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _raw_stream() -> int:
-    """The current stream of the current device as an integer: torch.cuda.current_stream() builds a Stream object
-    first, which takes longer (3.1 us) than the rest of a prepared call's way to the library."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+def _raw_stream(device: int) -> int:
+    """A device's current stream as an integer: torch.cuda.current_stream() builds a Stream object first, which takes
+    longer (3.1 us) than the rest of a prepared call's way to the library."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _stream(stream):
@@ -264,13 +264,17 @@ class PreparedCall:
     shape, dtype, device and storage, while it is used; their contents may change between calls. Calling it passes
     the given CUDA stream (default: the current one) and raises SegPagedError on a negative return code."""
 
-    __slots__ = ("_fn", "_name", "_args", "_keep")
+    __slots__ = ("_fn", "_name", "_args", "_keep", "_device")
 
     def __init__(self, fn, name: str, args: tuple, keep: tuple):
         self._fn, self._name, self._args, self._keep = fn, name, args, keep
+        self._device = torch.cuda.current_device()   # the library launches on the current device
 
     def __call__(self, stream=None):
-        r = self._fn(*self._args, _raw_stream() if stream is None else stream.cuda_stream)
+        if torch.cuda.current_device() != self._device:
+            raise ValueError(f"{self._name}: prepared on cuda:{self._device}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        r = self._fn(*self._args, _raw_stream(self._device) if stream is None else stream.cuda_stream)
         if r < 0:
             raise SegPagedError(r, self._name)
 

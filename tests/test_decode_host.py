@@ -126,6 +126,8 @@ def test_refusals_of_each_call():
         assert _call("segpaged_attn_decode", **{a: None}) == NULL
     for a in ("q", "o", "ws"):
         assert _call("segpaged_attn_decode", **{a: P8}) == ALIGN
+    for bad in (float("nan"), float("inf")):
+        assert _call("segpaged_attn_decode", scale=bad) == DIMS
     assert _call("segpaged_attn_decode", ws_bytes=16) == CAPACITY and _call("segpaged_attn_decode", tlen=-1) == DIMS
     assert sp.error_string(FORMAT).startswith("a pool format")
 
@@ -158,7 +160,11 @@ def test_binding_refuses_mismatched_tensors(monkeypatch):
                 kv_scale=_Fake((10, 2, 16), u8), page_table=_Fake((8,), i32), page_table_offs=_Fake((5,), i32),
                 ctx_len=_Fake((2,), i32), q_len=None, cls=_Fake((12,), i32), softmax_scale=0.1, o=_Fake((2, 8, 64), bf),
                 lse=_Fake((8, 2), torch.float32), workspace=_Fake((1 << 20,), u8))
-    sp.prepare_attn_decode(dims, **good)
+    call = sp.prepare_attn_decode(dims, **good)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)         # made for cuda:0, used while cuda:1 is current
+    with pytest.raises(ValueError, match="prepared on cuda:0"):
+        call()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     bad = dict(q=_Fake((2, 7, 64), bf), k_pool=_Fake((10, 16, 64), torch.float16), v_pool=_Fake((10, 16, 64), torch.int8),
                kv_scale=_Fake((10, 16), u8), page_table=_Fake((8,), torch.int64), page_table_offs=_Fake((4,), i32),
                ctx_len=_Fake((1,), i32), q_len=_Fake((1,), i32), cls=_Fake((11,), i32), o=_Fake((2, 8, 64), torch.float16),

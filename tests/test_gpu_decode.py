@@ -202,7 +202,8 @@ def test_decode_matches_oracle_with_nan_in_every_hidden_row(name, fmt):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("k_scale,v_scale,scale", [(8.0, 1.0, 0.5), (1e-3, 1e3, 1.0), (2.0 ** 20, 2.0 ** -60, 2.0 ** -22),
-                                                   (2.0 ** -40, 2.0 ** 60, 2.0 ** 37), (1.0, 1.0, 0.0), (1.0, 1.0, -0.3)])
+                                                   (2.0 ** -40, 2.0 ** 60, 2.0 ** 37), (1.0, 1.0, 0.0), (1.0, 1.0, -0.3),
+                                                   (1.0, 2.0 ** -114, 0.1), (1.0, 2.0 ** 122, 0.1), (100.0, 1.0, 0.09)])
 def test_decode_ranges(fmt, k_scale, v_scale, scale):
     """One-hot softmaxes, uniform ones, keys and values far from 1, a negative scale."""
     ly = Layer([(777, 1), (2050, 1)], 8, 2, 128, 32, [[GLOBAL, local(20, 200)]] * 2, fmt, seed=32, k_scale=k_scale,
@@ -382,3 +383,102 @@ def test_bad_tables_set_status_and_stay_in_bounds(fmt):
     t = ly.upload()
     _append(ly, t, bf16(np.ones((302, 2, 64))), bf16(np.ones((302, 2, 64))), [0, 1, 302])   # 301 rows, 300 tokens
     assert int(t["status"].item()) == sp.STATUS_TABLE
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tables_inside_a_larger_array(fmt):
+    """Offsets that begin past 0 and end before the table does: the entries around them belong to no head."""
+    ly = Layer([(300, 7), (65, 65)], 4, 2, 64, 32, [[GLOBAL, local(5, 40)], [local(0, 9), GLOBAL]], fmt, seed=40, spare=8)
+    spare = np.setdiff1d(np.arange(ly.num_pages), ly.table)[:5]
+    want, used = ly.expected_pools()
+    t = ly.upload(poison=False)
+    inner = t["table"]
+    t["table"] = i32(np.concatenate([spare[:3], ly.table, spare[3:]]))
+    t["offs"] += 3
+    o, lse = ly.decode(t)
+    check_attention(o, lse, ly.attention(0.125), fmt)
+    if fmt != "bf16":
+        k, v, sc = marked_pools(ly)
+        sp.segpaged_build_quant(ly.dims(), dev_bf16(ly.k), dev_bf16(ly.v), i32(ly.cu), t["lq"], t["cls"], t["table"],
+                                t["offs"], None, k, v, sc, t["status"])
+        _check_pools(ly, k, v, sc, want, used)
+        ko, vo, _ = marked_pools(ly, "bf16")
+        sp.segpaged_pages_dequant(ly.dims(), t["ctx"], t["lq"], t["cls"], t["table"], t["offs"], t["k"], t["v"], t["scale"],
+                                  ko, vo, t["status"])
+        assert (ko.float().cpu().numpy()[~used] == 5.0).all() and not (ko.float().cpu().numpy()[used] == 5.0).all()
+    _append(ly, t, ly.k[-2:], ly.v[-2:], [0, 0, 2])                       # the rows sequence 1 already ends with
+    assert int(t["status"].item()) == 0
+    for which, pool in enumerate((t["k"], t["v"])):
+        np.testing.assert_array_equal(raw(pool)[used], want[which][0][used])
+    assert torch.equal(inner, t["table"][3:-2])
+
+
+def test_two_graphs_take_turns_on_one_workspace():
+    """Graphs of two different layers captured over the same workspace and replayed one after the other, in any order."""
+    a, b = Layer(*SHAPES["one-long"], "e4m3", seed=41), Layer(*SHAPES["long-beside-short"], "e4m3", seed=42)
+    ws = torch.full((max(len(a.workspace()), len(b.workspace())),), 0xff, dtype=torch.uint8, device="cuda")
+    ts, graphs = [x.upload() for x in (a, b)], []
+    for x, t in zip((a, b), ts):
+        x.decode(t, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, capture_error_mode="thread_local"):
+            x.decode(t, workspace=ws)
+        graphs.append(g)
+    for order in ((0, 1), (1, 0, 0, 1), (1, 1, 0)):
+        for t in ts:
+            t["o"].fill_(9.0)
+            t["lse"].fill_(9.0)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for x, t in zip((a, b), ts):
+            check_attention(t["o"], t["lse"], x.attention(1.0 / math.sqrt(x.D)), str(order))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_pages_shared_by_heads_and_sequences(fmt):
+    """Two sequences with the same prefix whose tables name the same pages, and one head's table used by another."""
+    ly = Layer([(96, 1), (96, 1)], 4, 2, 64, 16, [[GLOBAL, GLOBAL]] * 2, fmt, seed=43)
+    t = ly.upload()
+    n = len(ly.table) // 4
+    for other in (1, 2, 3):
+        ly.table[other * n:(other + 1) * n] = ly.table[:n]
+    t["table"] = i32(ly.table)
+    o, lse = ly.decode(t)
+    ly.k[:, 1] = ly.k[:, 0]
+    ly.v[:, 1] = ly.v[:, 0]
+    ly.k[96:], ly.v[96:] = ly.k[:96], ly.v[:96]
+    check_attention(o, lse, ly.attention(0.125), fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_lengths_that_change_between_replays_to_empty_and_back(fmt):
+    """A captured call replayed with a sequence's slot emptied, filled again and the batch all empty."""
+    full = [(513, 1), (40, 1), (2000, 1)]
+    cls = [[GLOBAL, local(5, 100)]] * 3
+    ly = Layer(full, 8, 2, 64, 32, cls, fmt, seed=44)
+    t = ly.upload(poison=False)
+    ws = ly.workspace()
+    ly.decode(t, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="thread_local"):
+        ly.decode(t, workspace=ws)
+    want = ly.attention(0.125)
+    per = np.diff(ly.offs).reshape(3, 2)
+    flat = np.split(ly.table, ly.offs[1:-1])
+    for live in ([1], [0, 1, 2], [], [2], [0, 2], [0, 1, 2]):
+        keep = np.array([b in live for b in range(3)])
+        t["ctx"].copy_(i32(np.where(keep, ly.L, 0)))
+        t["lq"].copy_(i32(np.where(keep, ly.lq, 0)))
+        t["offs"].copy_(i32(np.concatenate([[0], np.cumsum((per * keep[:, None]).reshape(-1))])))
+        table = np.concatenate([flat[2 * b + h] for b in live for h in range(2)] or [np.zeros(0, np.int32)])
+        t["table"][:len(table)].copy_(i32(table))
+        t["o"].fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(t["status"].item()) == 0
+        o, lse, to, tl = (x.copy() for x in want)
+        o[~keep], lse[:, ~keep], to[~keep] = 0, -np.inf, 0
+        check_attention(t["o"], t["lse"], (o, lse, to, tl), str(live))
