@@ -193,6 +193,10 @@ __global__ void __launch_bounds__(32) append_kernel(AppendParams p) {
   const int32_t r = (int32_t)blockIdx.x, lane = threadIdx.x, c = lane % LANES;
   const int32_t kh = (int32_t)blockIdx.y * HEADS + lane / LANES;
   bool ok = kh < p.Hkv;
+  // Launched while the work before it may still run, and letting the attention that follows get ready meanwhile (which
+  // waits for this kernel's end before it reads anything).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   RowPiece k, v;
   k.lo = k.hi = v.lo = v.hi = make_uint4(0, 0, 0, 0);
   if (ok) {  // issued before the page look-up, whose loads depend on one another

@@ -57,9 +57,26 @@ void launch_build_quant(const BuildQuantParams& p, int grid, cudaStream_t st) {
   else build_quant_kernel<D, FMT, false><<<grid, 32 * kSliceWarps, 0, st>>>(p);
 }
 
+// A launch that may start while the work before it ends; the kernel waits for that before it reads or writes anything,
+// so that only its set-up overlaps the last blocks of what came before.
+template <typename... Params, typename... Args>
+int launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA;
+}
+
 template <int D, int FMT>
-void launch_append(const AppendParams& p, cudaStream_t st) {
-  append_kernel<D, FMT><<<dim3(p.total_new, (unsigned)ceil_div(p.Hkv, 512 / D)), 32, 0, st>>>(p);
+int launch_append(const AppendParams& p, cudaStream_t st) {
+  return launch_early(append_kernel<D, FMT>, dim3(p.total_new, (unsigned)ceil_div(p.Hkv, 512 / D)), 32, 0, st, p);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -93,23 +110,9 @@ int launch_decode_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeP
       return SEGPAGED_ERR_CUDA;
     configured[dev].store(true, std::memory_order_release);
   }
-  // Both launches may start while the work before them ends (each waits for that before it reads or writes anything):
-  // their set-up overlaps its last blocks.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM_BYTES;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, decode_kernel<D, FMT, NB>, tk, tv, p) != cudaSuccess) return SEGPAGED_ERR_CUDA;
-  cfg.gridDim = dim3(grid, std::min(p.G, kDecodeGroup));
-  cfg.blockDim = dim3(32 * kDecodeCombineWarps);
-  cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, decode_combine_kernel<D>, p) != cudaSuccess) return SEGPAGED_ERR_CUDA;
+  if (launch_early(decode_kernel<D, FMT, NB>, dim3(grid), C::THREADS, C::SMEM_BYTES, st, tk, tv, p)) return SEGPAGED_ERR_CUDA;
+  if (launch_early(decode_combine_kernel<D>, dim3(grid, std::min(p.G, kDecodeGroup)), 32 * kDecodeCombineWarps, 0, st, p))
+    return SEGPAGED_ERR_CUDA;
   return launched();
 }
 
@@ -193,7 +196,7 @@ extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, con
                                const int32_t* q_len, const segpaged_head_class* cls, const int32_t* page_table,
                                int64_t page_table_len, const int32_t* page_table_offs, void* k_pool, void* v_pool,
                                uint8_t* kv_scale, int32_t* status, void* stream) {
-  const int rc = check_pools(dims, kv_format, true, k_pool, v_pool, kv_scale);
+  int rc = check_pools(dims, kv_format, true, k_pool, v_pool, kv_scale);
   if (rc) return rc;
   if (total_new < 0 || page_table_len < 0) return SEGPAGED_ERR_DIMS;
   if (dims->num_seqs == 0 || total_new == 0) return SEGPAGED_OK;
@@ -220,8 +223,8 @@ extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, con
   p.log2_page = log2_int(dims->page_size);
   p.num_pages = dims->num_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SEGPAGED_BY_SHAPE(launch_append, (p, st));
-  return launched();
+  SEGPAGED_BY_SHAPE(rc = launch_append, (p, st));
+  return rc == SEGPAGED_OK ? launched() : rc;
 }
 
 namespace {
