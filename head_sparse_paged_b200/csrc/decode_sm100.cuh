@@ -312,8 +312,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     ptx::tmem_relinquish();
   }
   // The launch may start while the one before it ends; nothing it wrote is read, and nothing written, before this.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  early_start();
 
   // ---- this CTA's run of tiles. The work is counted in half tiles: a pair of n tiles is 2 n + PAIR_COST of them, and
   // a CTA takes the tiles that begin in its equal share of the sum. Thread i adds up pairs [i * per, (i + 1) * per).
@@ -1029,8 +1028,7 @@ __global__ void __launch_bounds__(32 * kDecodeCombineWarps, 5) decode_combine_ke
   __shared__ float s_lse[kDecodeMaxCtas], s_sum[NW], s_top[NW], s_o[NW][D];
   const int32_t cta = blockIdx.x, head = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results of the launch before this one
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  early_start();  // the partial results of the launch before this one
   const int2 meta = *reinterpret_cast<const int2*>(p.part_meta + 2 * cta);
   const int32_t pair = meta.x, n = min(meta.y, kDecodeMaxCtas);
   if (n <= 1) return;

@@ -94,6 +94,13 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c, int half, const
   *reinterpret_cast<uint2*>(row + half + 8 * c) = hi;
 }
 
+// For kernels that may be launched while the work before them still runs: waits for its end, before anything is read or
+// written, and lets the launch after this one get ready meanwhile.
+__device__ __forceinline__ void early_start() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 struct BuildQuantParams {
   BuildParams b;       // k_pool, v_pool unused
   uint8_t* k_pool;     // [num_pages][P][D] codes
@@ -108,6 +115,7 @@ __global__ void __launch_bounds__(32 * kSliceWarps) build_quant_kernel(BuildQuan
   const BuildParams& p = q.b;
   constexpr int LANES = D / 16, ROWS = 32 / LANES, N = kSliceRows / ROWS;  // lanes of a row, rows a pass, passes
   const int lane = threadIdx.x & 31, c = lane % LANES;
+  early_start();
   const int nheads = p.B * p.Hkv, log2_slices = q.log2_page - kLog2SliceRows;
   const int64_t slices = q.table_len << log2_slices, begin = p.offs[0], entries = p.offs[nheads];
   if (blockIdx.x == 0 && threadIdx.x == 0 && entries > q.table_len) report(p.status, 2);
@@ -193,10 +201,7 @@ __global__ void __launch_bounds__(32) append_kernel(AppendParams p) {
   const int32_t r = (int32_t)blockIdx.x, lane = threadIdx.x, c = lane % LANES;
   const int32_t kh = (int32_t)blockIdx.y * HEADS + lane / LANES;
   bool ok = kh < p.Hkv;
-  // Launched while the work before it may still run, and letting the attention that follows get ready meanwhile (which
-  // waits for this kernel's end before it reads anything).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  early_start();
   RowPiece k, v;
   k.lo = k.hi = v.lo = v.hi = make_uint4(0, 0, 0, 0);
   if (ok) {  // issued before the page look-up, whose loads depend on one another
@@ -291,6 +296,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(32 * kSliceWarps) dequant_pages_kernel(DequantParams p) {
   constexpr int LANES = D / 8, ROWS = 32 / LANES, N = kSliceRows / ROWS;
   const int lane = threadIdx.x & 31, c = lane % LANES;
+  early_start();
   const int nheads = p.B * p.Hkv, log2_slices = p.log2_page - kLog2SliceRows;
   const int64_t slices = p.table_len << log2_slices, begin = p.offs[0], entries = p.offs[nheads];
   const int64_t warps = (int64_t)gridDim.x * kSliceWarps;

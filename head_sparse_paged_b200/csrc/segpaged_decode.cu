@@ -45,18 +45,6 @@ int sm_count() {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA; }
 
-// Blocks of the kernels that take a slice of a page a warp: a warp for each slice (the kernels loop past the limit).
-int slice_blocks(int64_t table_len, int log2_page) {
-  const int64_t per_page = (1 << log2_page) / kSliceRows;
-  return (int)std::min<int64_t>(ceil_div(std::min<int64_t>(table_len, INT32_MAX) * per_page, kSliceWarps), 1 << 22);
-}
-
-template <int D, int FMT>
-void launch_build_quant(const BuildQuantParams& p, int grid, cudaStream_t st) {
-  if (p.b.cos_sin) build_quant_kernel<D, FMT, true><<<grid, 32 * kSliceWarps, 0, st>>>(p);
-  else build_quant_kernel<D, FMT, false><<<grid, 32 * kSliceWarps, 0, st>>>(p);
-}
-
 // A launch that may start while the work before it ends; the kernel waits for that before it reads or writes anything,
 // so that only its set-up overlaps the last blocks of what came before.
 template <typename... Params, typename... Args>
@@ -72,6 +60,18 @@ int launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA;
+}
+
+// Blocks of the kernels that take a slice of a page a warp: a warp for each slice (the kernels loop past the limit).
+int slice_blocks(int64_t table_len, int log2_page) {
+  const int64_t per_page = (1 << log2_page) / kSliceRows;
+  return (int)std::min<int64_t>(ceil_div(std::min<int64_t>(table_len, INT32_MAX) * per_page, kSliceWarps), 1 << 22);
+}
+
+template <int D, int FMT>
+int launch_build_quant(const BuildQuantParams& p, int grid, cudaStream_t st) {
+  return p.b.cos_sin ? launch_early(build_quant_kernel<D, FMT, true>, dim3(grid), 32 * kSliceWarps, 0, st, p)
+                     : launch_early(build_quant_kernel<D, FMT, false>, dim3(grid), 32 * kSliceWarps, 0, st, p);
 }
 
 template <int D, int FMT>
@@ -159,7 +159,7 @@ extern "C" int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format
                                     const int32_t* page_table, int64_t page_table_len, const int32_t* page_table_offs,
                                     const float* rope_cos_sin, void* k_pool, void* v_pool, uint8_t* kv_scale,
                                     int32_t* status, void* stream) {
-  const int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
+  int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
   if (rc) return rc;
   if (page_table_len < 0) return SEGPAGED_ERR_DIMS;
   if (dims->num_seqs == 0 || page_table_len == 0) return SEGPAGED_OK;
@@ -187,8 +187,8 @@ extern "C" int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format
   p.table_len = page_table_len;
   p.log2_page = log2_int(dims->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SEGPAGED_BY_SHAPE_8BIT(launch_build_quant, (p, slice_blocks(page_table_len, p.log2_page), st));
-  return launched();
+  SEGPAGED_BY_SHAPE_8BIT(rc = launch_build_quant, (p, slice_blocks(page_table_len, p.log2_page), st));
+  return rc == SEGPAGED_OK ? launched() : rc;
 }
 
 extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, const void* k_new, const void* v_new,
@@ -229,8 +229,8 @@ extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, con
 
 namespace {
 template <int D, int FMT>
-void launch_dequant(const DequantParams& p, int grid, cudaStream_t st) {
-  dequant_pages_kernel<D, FMT><<<grid, 32 * kSliceWarps, 0, st>>>(p);
+int launch_dequant(const DequantParams& p, int grid, cudaStream_t st) {
+  return launch_early(dequant_pages_kernel<D, FMT>, dim3(grid), 32 * kSliceWarps, 0, st, p);
 }
 }  // namespace
 
@@ -239,7 +239,7 @@ extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_form
                                       int64_t page_table_len, const int32_t* page_table_offs, const void* k_pool,
                                       const void* v_pool, const uint8_t* kv_scale, void* k_out, void* v_out,
                                       int32_t* status, void* stream) {
-  const int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
+  int rc = check_pools(dims, kv_format, false, k_pool, v_pool, kv_scale);
   if (rc) return rc;
   if (page_table_len < 0) return SEGPAGED_ERR_DIMS;
   if (dims->num_seqs == 0 || page_table_len == 0) return SEGPAGED_OK;
@@ -263,8 +263,8 @@ extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_form
   p.log2_page = log2_int(dims->page_size);
   p.num_pages = dims->num_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SEGPAGED_BY_SHAPE_8BIT(launch_dequant, (p, slice_blocks(page_table_len, p.log2_page), st));
-  return launched();
+  SEGPAGED_BY_SHAPE_8BIT(rc = launch_dequant, (p, slice_blocks(page_table_len, p.log2_page), st));
+  return rc == SEGPAGED_OK ? launched() : rc;
 }
 
 // Per CTA the two chunks its run can start and end with, and which pair goes on behind it.
