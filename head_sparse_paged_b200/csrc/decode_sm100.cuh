@@ -75,6 +75,7 @@ struct DecodeParams {
   int64_t table_len;
   int32_t B, Hkv, G, log2_page, num_pages;
   int32_t log2_hg;             // passes of a group: max(1, G / 16)
+  int32_t whole;               // no pair is cut: each is done by the CTA whose share its first unit lies in
   float scale_log2;
 };
 
@@ -356,7 +357,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     if (per > 1) own = decode_pair(p, u);
     const int32_t n = own.g.n;
     const uint32_t at = 2u * rank + (uint32_t)C::PAIR_COST * u, next = at + 2u * n + C::PAIR_COST;
-    if (takes_part && lo_unit >= at && lo_unit < next) {
+    if (p.whole) {
+      // (the pair after this one is a run's first if the share begins inside this one or at its end)
+      if (takes_part && lo_unit > at && lo_unit <= next) {
+        sm.pair0 = u + 1;
+        sm.first_rank = rank + n;
+      }
+      if (takes_part && hi_unit > at && hi_unit <= next) sm.end_rank = rank + n;
+    } else if (takes_part && lo_unit >= at && lo_unit < next) {
       const int32_t tile = min(n, (int32_t)(lo_unit - at + 1) / 2);
       sm.pair0 = u;
       sm.tile0 = tile;
@@ -368,7 +376,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + own.off + (page < own.n_sink ? page : page - own.w0 + own.n_sink)));
       }
     }
-    if (takes_part && hi_unit > at && hi_unit <= next) sm.end_rank = rank + min(n, (int32_t)(hi_unit - at + 1) / 2);
+    if (!p.whole && takes_part && hi_unit > at && hi_unit <= next) sm.end_rank = rank + min(n, (int32_t)(hi_unit - at + 1) / 2);
     rank += n;
     // a pair without a visible key (an empty sequence): O = 0, LSE = -inf, written by one CTA
     if (own.g.L == 0 && u % gridDim.x == cta) {

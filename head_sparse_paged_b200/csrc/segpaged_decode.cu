@@ -98,6 +98,12 @@ bool encode_pool(CUtensorMap* map, const void* base, int P, int64_t pages) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Where all the tables together hold no more tokens than this, no (sequence, KV head) is cut into chunks and nothing is left
+// to join: even if they are all one pair's, its tiles one after the other take no longer than the second launch. One head
+// of 256, 512, 640, 768 tokens (D = 128, e4m3, replayed graphs): 8.1, 9.3, 9.8, 10.3 us whole, 9.9, 10.0, 10.1, 10.0 us
+// cut and joined; eight heads of 64: 7.4 against 9.0 us. bf16 and D = 64 cross at or above 640 too.
+constexpr int64_t kDecodeWholeTokens = 640;
+
 template <int D, int FMT, int NB>
 int launch_decode_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int grid, cudaStream_t st) {
   using C = DecodeCfg<D, FMT, NB>;
@@ -111,7 +117,7 @@ int launch_decode_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeP
     configured[dev].store(true, std::memory_order_release);
   }
   if (launch_early(decode_kernel<D, FMT, NB>, dim3(grid), C::THREADS, C::SMEM_BYTES, st, tk, tv, p)) return SEGPAGED_ERR_CUDA;
-  if (launch_early(decode_combine_kernel<D>, dim3(grid, std::min(p.G, kDecodeGroup)), 32 * kDecodeCombineWarps, 0, st, p))
+  if (!p.whole && launch_early(decode_combine_kernel<D>, dim3(grid, std::min(p.G, kDecodeGroup)), 32 * kDecodeCombineWarps, 0, st, p))
     return SEGPAGED_ERR_CUDA;
   return launched();
 }
@@ -311,6 +317,7 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   p.log2_page = log2_int(dims->page_size);
   p.num_pages = dims->num_pages;
   p.log2_hg = p.G > kDecodeGroup ? log2_int(p.G / kDecodeGroup) : 0;
+  p.whole = page_table_len <= kDecodeWholeTokens >> p.log2_page;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = SEGPAGED_OK;
