@@ -470,6 +470,12 @@ def prepare_build_quant(dims: Dims, k_dense, v_dense, cu_seqlens_k, q_len, cls, 
     bf = torch.bfloat16
     d = dims.c()
     fmt, kp, vp, ks = _pools(dims, k_pool, v_pool, kv_scale)
+    heads = dims.num_seqs * dims.num_kv_heads
+    for t, need, what in ((v_dense, k_dense.numel(), "v_dense"), (cu_seqlens_k, dims.num_seqs + 1, "cu_seqlens_k"),
+                          (q_len, dims.num_seqs, "q_len"), (cls, 3 * heads, "cls"),
+                          (page_table_offs, heads + 1, "page_table_offs"),
+                          (rope_cos_sin, dims.num_seqs * dims.head_dim, "rope_cos_sin")):
+        _size(t, need, what)
     args = (ctypes.byref(d), fmt, _dev(k_dense, bf, "k_dense"), _dev(v_dense, bf, "v_dense"),
             _dev(cu_seqlens_k, torch.int32, "cu_seqlens_k"), _dev(q_len, torch.int32, "q_len"),
             _dev(cls, torch.int32, "cls"), _dev(page_table, torch.int32, "page_table"), int(page_table.numel()),

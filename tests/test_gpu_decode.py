@@ -482,3 +482,44 @@ def test_lengths_that_change_between_replays_to_empty_and_back(fmt):
         o, lse, to, tl = (x.copy() for x in want)
         o[~keep], lse[:, ~keep], to[~keep] = 0, -np.inf, 0
         check_attention(t["o"], t["lse"], (o, lse, to, tl), str(live))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(fmt):
+    """Page ids whose rows lie beyond 2^31 elements (and bytes) of the pools: every call, against the same pages at 0."""
+    ly = Layer([(700, 3), (129, 1)], 16, 2, 128, 128, [[GLOBAL, local(20, 200)]] * 2, fmt, seed=45)
+    first = (1 << 31) // (ly.P * ly.D) + 3
+    t = ly.upload()
+    small = {k: t[k] for k in ("k", "v", "scale")}
+    dims = sp.Dims(ly.B, ly.hq, ly.hkv, ly.D, ly.P, first + ly.num_pages)
+
+    def big(x, rows):
+        out = torch.empty((dims.num_pages, *rows), dtype=x.dtype, device="cuda")
+        out[first:].copy_(x)
+        return out
+
+    k, v = (big(small[x].view(torch.uint8) if fmt != "bf16" else small[x], (ly.P, ly.D)).view(small[x].dtype) for x in "kv")
+    sc = None if fmt == "bf16" else big(small["scale"], (2, ly.P))
+    table = t["table"] + first
+    seq = (t["ctx"], t["lq"], t["cls"], table, t["offs"])
+    ws = torch.empty(sp.segpaged_decode_workspace_bytes(dims), dtype=torch.uint8, device="cuda")
+    sp.segpaged_attn_decode(dims, t["q"], k, v, sc, table, t["offs"], t["ctx"], t["lq"], t["cls"], 0.09, t["o"], t["lse"], ws,
+                            t["status"])
+    check_attention(t["o"], t["lse"], ly.attention(0.09), fmt)
+    want, used = ly.expected_pools()
+    sp.segpaged_append(dims, dev_bf16(ly.k[[699, 828]]), dev_bf16(ly.v[[699, 828]]), i32([0, 1, 2]), *seq, k, v, sc, t["status"])
+    cut = lambda x: x.view(torch.uint8)[first:] if x.dtype != torch.bfloat16 else x[first:]  # noqa: E731
+    see = ly.visible_pool_rows()
+    for which, x in enumerate((k, v)):
+        np.testing.assert_array_equal(raw(cut(x))[see], want[which][0][see])
+    if fmt != "bf16":
+        out = [torch.empty(dims.num_pages, ly.P, ly.D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        sp.segpaged_pages_dequant(dims, *seq, k, v, sc, *out, t["status"])
+        for which, x in enumerate(out):
+            ref = orc.dequantise_rows(*want[which], fmt)
+            np.testing.assert_array_equal(x[first:].float().cpu().numpy()[see], ref[see])
+        k.view(torch.uint8)[first:] = 0
+        sp.segpaged_build_quant(dims, dev_bf16(ly.k), dev_bf16(ly.v), i32(ly.cu), t["lq"], t["cls"], table, t["offs"], None, k, v,
+                                sc, t["status"])
+        np.testing.assert_array_equal(raw(cut(k))[see] & 127, want[0][0][see] & 127)
+    assert int(t["status"].item()) == 0
