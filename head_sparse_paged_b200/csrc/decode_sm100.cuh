@@ -95,11 +95,14 @@ struct DecodeCfg {
   static constexpr int BLOCK_BYTES = kDecodeTile * ROWB;
   static constexpr int TILE_BYTES = CB * BLOCK_BYTES;            // K or V
   static constexpr int SCALE_BYTES = FMT == kFmtBf16 ? 0 : 2 * kDecodeTile;
-  static constexpr int Q_BYTES = NB * 8 * D * 2;
+  // A query row takes 16 bytes more than it holds, so that the eight rows that a fragment load touches lie in different
+  // banks: without them the twelve warps' loads take 1536 cycles of shared memory at the start of each chunk.
+  static constexpr int Q_ROW = D * 2 + 16;
+  static constexpr int Q_BYTES = NB * 8 * Q_ROW;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int EXTRA_BYTES = SCALE_BYTES + Q_BYTES;      // beside a stage: exponent bytes, query rows
   static constexpr int MERGE_BYTES = kDecodeHelpers * 8 * D * 4;  // a helper's sum of one column block of O
-  static constexpr int FIXED_BYTES = MERGE_BYTES + 4608 + 1024;  // + barriers and small arrays, alignment slack
+  static constexpr int FIXED_BYTES = MERGE_BYTES + 3840 + 1024;  // + barriers and small arrays, alignment slack
   static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
@@ -132,9 +135,12 @@ struct DecodeTileHeader {
   int32_t flags;    // bit 0: first tile of a chunk, bit 1: last; bits 2..: 1 + partial slot, 0: the whole pair
 };
 
-// Tiles of one (sequence, KV head): [0, n_a) cover tokens [0, a1), the others [b0, L) of which [lo, L) are visible.
+// Tiles of one (sequence, KV head), n of them: the first n_a cover tokens [0, a1), the others those from b0, the start of
+// lo's page, of which [lo, L) are visible.
 struct DecodeGeom {
-  int32_t L, a1, b0, lo, n_a, n;
+  int32_t L, a1, lo, n;
+  __device__ __forceinline__ int32_t n_a() const { return (a1 + kDecodeTile - 1) / kDecodeTile; }
+  __device__ __forceinline__ int32_t b0(int32_t log2_page) const { return lo >> log2_page << log2_page; }
 };
 // A pair: those tiles, the outputs they go to, and the page table: entries [off, off + len), logical page lp at entry lp
 // below n_sink and at lp - w0 + n_sink from there on.
@@ -159,9 +165,7 @@ __device__ __forceinline__ DecodePair decode_pair(const DecodeParams& p, int32_t
   r.g.lo = max(L - hp.window, 0);
   r.g.a1 = hp.sink;
   if (hp.global || hp.sink >= r.g.lo) r.g.a1 = r.g.lo = 0;  // one run of visible tokens
-  r.g.b0 = (r.g.lo >> lp) << lp;
-  r.g.n_a = (r.g.a1 + kDecodeTile - 1) / kDecodeTile;
-  r.g.n = r.g.n_a + (int32_t)(((uint32_t)(L - r.g.b0) + kDecodeTile - 1) / kDecodeTile);
+  r.g.n = r.g.n_a() + (int32_t)(((uint32_t)(L - r.g.b0(lp)) + kDecodeTile - 1) / kDecodeTile);
   // A table that does not hold exactly these pages: the pair is reported and left out.
   if (L > 0 && (r.len != hp.total || r.off < 0 || r.off > p.table_len - r.len)) {
     report(p.status, 2);
@@ -275,7 +279,7 @@ struct DecodeSmall {
   uint32_t tmem;
   DecodePair window[32];                        // pairs pair0 ..
 };
-static_assert(sizeof(DecodeSmall) <= 4608, "small shared arrays");
+static_assert(sizeof(DecodeSmall) <= 3840, "small shared arrays");
 
 template <int D, int FMT, int NB>
 __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
@@ -370,8 +374,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       sm.tile0 = tile;
       sm.first_rank = rank + tile;
       if (tile < n) {  // the run's first page ids will be wanted in a moment
-        const int64_t tok = tile < own.g.n_a ? (int64_t)tile * kDecodeTile
-                                             : own.g.b0 + (int64_t)(tile - own.g.n_a) * kDecodeTile;
+        const int32_t n_a = own.g.n_a();
+        const int64_t tok = tile < n_a ? (int64_t)tile * kDecodeTile
+                                       : own.g.b0(p.log2_page) + (int64_t)(tile - n_a) * kDecodeTile;
         const int32_t page = (int32_t)(tok >> p.log2_page);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + own.off + (page < own.n_sink ? page : page - own.w0 + own.n_sink)));
       }
@@ -459,8 +464,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       for (int d = 16; d > 0; d >>= 1)
         if (__shfl_sync(0xffffffffu, w_end, k + d - 1) <= i) k += d;
       const int32_t n = __shfl_sync(0xffffffffu, w.g.n, k), end_k = __shfl_sync(0xffffffffu, w_end, k);
-      const int32_t n_a = __shfl_sync(0xffffffffu, w.g.n_a, k), b0 = __shfl_sync(0xffffffffu, w.g.b0, k);
       const int32_t a1 = __shfl_sync(0xffffffffu, w.g.a1, k), lo_k = __shfl_sync(0xffffffffu, w.g.lo, k);
+      const int32_t n_a = (a1 + kDecodeTile - 1) / kDecodeTile, b0 = lo_k & -page;
       const int32_t L = __shfl_sync(0xffffffffu, w.g.L, k), off = __shfl_sync(0xffffffffu, w.off, k);
       const int32_t sink = __shfl_sync(0xffffffffu, w.n_sink, k);
       const int32_t w0 = __shfl_sync(0xffffffffu, w.w0, k);
@@ -645,15 +650,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           uint8_t* extra = extras + s * C::EXTRA_BYTES;
           const bool load = my_tile == at_box && cur.need;
           const uint32_t have = __ballot_sync(0xffffffffu, load);
-          if (lane == at_box * boxes) {
-            const bool with_q = cur.h.flags & 1;
+          const int leader = at_box * boxes;
+          const bool with_q = __shfl_sync(0xffffffffu, cur.h.flags, leader) & 1;
+          if (lane == leader) {
             sm.hdr[s] = cur.h;
             ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + (with_q ? heads * D * 2 : 0));
-            if (with_q)
-              bulk_load(extra + C::SCALE_BYTES, p.q + ((int64_t)cur.h.b * Hq + cur.h.h0) * D, heads * D * 2, &sm.full[s]);
           }
           issued = i;
           __syncwarp();
+          if (with_q) {
+            const int64_t row = (int64_t)__shfl_sync(0xffffffffu, cur.h.b, leader) * Hq + __shfl_sync(0xffffffffu, cur.h.h0, leader);
+            if (lane < heads)
+              bulk_load(extra + C::SCALE_BYTES + lane * C::Q_ROW, p.q + (row + lane) * D, D * 2, &sm.full[s]);
+          }
           if (load) {
 #pragma unroll
             for (int cb = 0; cb < C::CB; ++cb) {
@@ -745,7 +754,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       const uint8_t* extra = extras + s * C::EXTRA_BYTES;
       if (h.flags & 1) {
         // ---- a chunk begins: query fragments, running values
-        const __nv_bfloat16* qs = reinterpret_cast<const __nv_bfloat16*>(extra + C::SCALE_BYTES);
+        const uint8_t* qs = extra + C::SCALE_BYTES;
         vref = 0;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -757,19 +766,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             for (int j = 0; j < 2; ++j) {
               // fp16: the contraction runs in the order the code bytes lie in, 4t .. 4t+3 of each 16
               const int d = 16 * ks + (BF ? 2 * t + 8 * j : 4 * t + 2 * j);
-              qf[nb][ks][j] = head < heads ? *reinterpret_cast<const uint32_t*>(qs + head * D + d) : 0u;
-              if (p.scale_log2 < 0.f) qf[nb][ks][j] ^= 0x80008000u;
+              qf[nb][ks][j] = head < heads ? *reinterpret_cast<const uint32_t*>(qs + head * C::Q_ROW + 2 * d) : 0u;
+              if (BF) qf[nb][ks][j] ^= p.scale_log2 < 0.f ? 0x80008000u : 0u;
               top = absmax2(top, qf[nb][ks][j]);
             }
           }
           if (BF) {
             head_scale[nb][0] = head_scale[nb][1] = fmaxf(fabsf(p.scale_log2), kDecodeMinScale);
           } else {
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            top = max2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max2(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int32_t biased = (int32_t)(max(top & 0xffffu, top >> 16) >> 7);
             const int32_t e = biased == 255 ? 0 : 15 - max(biased - 127, -100);  // not finite: as it is
-            const float up = exp2_int(e);
+            const float up = copysignf(exp2_int(e), p.scale_log2);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll

@@ -78,7 +78,7 @@ __device__ __forceinline__ int32_t row_byte(const RowPiece& r) {
   uint32_t m = absmax2(absmax2(absmax2(absmax2(0u, r.lo.x), r.lo.y), r.lo.z), r.lo.w);
   m = absmax2(absmax2(absmax2(absmax2(m, r.hi.x), r.hi.y), r.hi.z), r.hi.w);
 #pragma unroll
-  for (int d = LANES / 2; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+  for (int d = LANES / 2; d > 0; d >>= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, d));
   return row_exponent_byte<FMT>(max(m & 0xffffu, m >> 16));
 }
 

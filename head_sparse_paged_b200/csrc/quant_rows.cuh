@@ -19,9 +19,15 @@ namespace segpaged {
 constexpr int kFmtBf16 = 0, kFmtE4m3 = 1, kFmtInt8 = 2;
 constexpr int kRowNaN = 255;  // exponent byte of a row with an infinity or a NaN
 
-// Largest magnitude of two packed bf16 pairs, as packed bf16 bit patterns: magnitudes order like their bits, and
-// infinities and NaNs (0x7f80 and above) order above every finite value.
-__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+// Larger of two bf16 pairs, each half by itself; a NaN (0x7fff) wins. (As an integer maximum of the bit patterns, which
+// magnitudes order like, it is several instructions: 1390 instead of 1160 cycles for the queries of a chunk.)
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Largest magnitude of two packed bf16 pairs: 0x7f80 and above for infinities and NaNs.
+__device__ __forceinline__ uint32_t absmax2(uint32_t m, uint32_t w) { return max2(m, w & 0x7fff7fffu); }
 
 // Exponent byte of a row whose largest magnitude has the bf16 bits `top`.
 template <int FMT>
