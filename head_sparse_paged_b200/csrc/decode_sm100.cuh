@@ -174,6 +174,33 @@ __device__ __forceinline__ DecodePair decode_pair(const DecodeParams& p, int32_t
   return r;
 }
 
+// First token of a tile and its visible tokens [lo, hi).
+struct DecodeSpan {
+  int32_t t0, lo, hi;
+};
+__device__ __forceinline__ DecodeSpan decode_span(const DecodeGeom& g, int32_t tile, int32_t log2_page) {
+  DecodeSpan s;
+  const int32_t n_a = g.n_a();
+  const bool in_sink = tile < n_a;
+  s.t0 = in_sink ? tile * kDecodeTile : g.b0(log2_page) + (tile - n_a) * kDecodeTile;
+  s.lo = max(s.t0, in_sink ? 0 : g.lo);
+  s.hi = (int32_t)min((int64_t)s.t0 + kDecodeTile, (int64_t)(in_sink ? g.a1 : g.L));
+  return s;
+}
+
+// The K and V copies of one box (up to 64 rows of a page): `at`, its first row in the stage's tiles; `row`, its first row in
+// the page.
+template <typename C>
+__device__ __forceinline__ void issue_box(uint8_t* stage, const CUtensorMap& tk, const CUtensorMap& tv, int32_t at, int32_t row,
+                                          int32_t page, uint64_t* bar) {
+#pragma unroll
+  for (int cb = 0; cb < C::CB; ++cb) {
+    uint8_t* to = stage + cb * C::BLOCK_BYTES + at * C::ROWB;
+    ptx::tma_load_3d(to, &tk, cb * (C::ROWB / C::EB), row, page, bar);
+    ptx::tma_load_3d(to + C::TILE_BYTES, &tv, cb * (C::ROWB / C::EB), row, page, bar);
+  }
+}
+
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -442,6 +469,27 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       bool need;        // a visible token lies in it
       DecodeTileHeader h;
     } cur, nxt;
+    // The header (but b and h0) of the run's tile i, which is tile `tile` of pair u's n; the pair ends before tile `pair_end` of
+    // the run. `say`: this lane leaves word of a chunk that the CTAs behind this one go on with.
+    auto header = [&](int32_t i, int32_t tile, int32_t n, int32_t u, int32_t pair_end, const DecodeSpan& sp, bool say) {
+      DecodeTileHeader h;
+      const bool last = i + 1 == tiles || tile + 1 == n;
+      h.rows = (sp.lo - sp.t0) | (sp.hi - sp.t0) << 16;
+      h.flags = (tile == 0 || i == 0 ? 1 : 0) | (last ? 2 : 0);
+      if (last) {
+        const bool from_start = tile <= i, to_end = tile + 1 == n;  // does the chunk hold the pair's first, last tile
+        if (!(from_start && to_end)) h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
+        if (say && from_start && !to_end) {
+          // the pair goes on in the CTAs after this one, to the CTA that holds its last tile
+          const uint32_t at = 2u * (first_rank + pair_end - 1) + (uint32_t)C::PAIR_COST * u;  // that tile's unit
+          const uint32_t wide = (share + 1) * spare;  // units of the CTAs that take one more
+          const int32_t to = at < wide ? at / (share + 1) : spare + (at - wide) / share;
+          p.part_meta[2 * cta] = u;
+          p.part_meta[2 * cta + 1] = to - cta + 1;
+        }
+      }
+      return h;
+    };
     // The boxes of tiles i0, i0 + kStep, ... into nxt; returns how many tiles that are (0: the run is done).
     auto plan = [&](int32_t i0) -> int32_t {
       nxt.need = false;
@@ -464,34 +512,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       for (int d = 16; d > 0; d >>= 1)
         if (__shfl_sync(0xffffffffu, w_end, k + d - 1) <= i) k += d;
       const int32_t n = __shfl_sync(0xffffffffu, w.g.n, k), end_k = __shfl_sync(0xffffffffu, w_end, k);
-      const int32_t a1 = __shfl_sync(0xffffffffu, w.g.a1, k), lo_k = __shfl_sync(0xffffffffu, w.g.lo, k);
-      const int32_t n_a = (a1 + kDecodeTile - 1) / kDecodeTile, b0 = lo_k & -page;
-      const int32_t L = __shfl_sync(0xffffffffu, w.g.L, k), off = __shfl_sync(0xffffffffu, w.off, k);
-      const int32_t sink = __shfl_sync(0xffffffffu, w.n_sink, k);
+      DecodeGeom g;
+      g.L = __shfl_sync(0xffffffffu, w.g.L, k);
+      g.a1 = __shfl_sync(0xffffffffu, w.g.a1, k);
+      g.lo = __shfl_sync(0xffffffffu, w.g.lo, k);
+      const int32_t off = __shfl_sync(0xffffffffu, w.off, k), sink = __shfl_sync(0xffffffffu, w.n_sink, k);
       const int32_t w0 = __shfl_sync(0xffffffffu, w.w0, k);
       const int32_t tile = i - (end_k - n);
-      const bool in_sink = tile < n_a;
-      const int32_t t0 = in_sink ? tile * kDecodeTile : b0 + (tile - n_a) * kDecodeTile;
-      const int32_t lo = max(t0, in_sink ? 0 : lo_k);
-      const int32_t hi = (int32_t)min((int64_t)t0 + kDecodeTile, (int64_t)(in_sink ? a1 : L));
-      const bool last = i + 1 == tiles || tile + 1 == n;
-      nxt.h.rows = (lo - t0) | (hi - t0) << 16;
+      const DecodeSpan sp = decode_span(g, tile, p.log2_page);
+      const int32_t t0 = sp.t0, lo = sp.lo, hi = sp.hi;
+      const bool mine = i0 + my_tile * kStep < stop;
+      nxt.h = header(i, tile, n, window + k, end_k, sp, mine && my_row == 0);
       nxt.h.b = __shfl_sync(0xffffffffu, w.b, k);
       nxt.h.h0 = __shfl_sync(0xffffffffu, w.h0, k);
-      nxt.h.flags = (tile == 0 || i == 0 ? 1 : 0) | (last ? 2 : 0);
-      const bool mine = i0 + my_tile * kStep < stop;
-      if (last) {
-        const bool from_start = tile <= i, to_end = tile + 1 == n;  // does the chunk hold the pair's first, last tile
-        if (!(from_start && to_end)) nxt.h.flags |= (1 + 2 * cta + (from_start ? 1 : 0)) << 2;
-        if (mine && from_start && !to_end && my_row == 0) {
-          // the pair goes on in the CTAs after this one, to the CTA that holds its last tile
-          const uint32_t at = 2u * (first_rank + end_k - 1) + (uint32_t)C::PAIR_COST * (window + k);  // its unit
-          const uint32_t wide = (share + 1) * spare;  // units of the CTAs that take one more
-          const int32_t to = at < wide ? at / (share + 1) : spare + (at - wide) / share;
-          p.part_meta[2 * cta] = window + k;
-          p.part_meta[2 * cta + 1] = to - cta + 1;
-        }
-      }
       const int64_t tok = (int64_t)t0 + my_row;
       nxt.need = mine && my_tile < batch_tiles && tok + box > lo && tok < hi;
       nxt.row = (int32_t)(tok & (page - 1));
@@ -501,6 +534,44 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         nxt.id = __ldg(p.table + off + (lp < sink ? lp : lp - w0 + sink));
       }
       return min(batch_tiles, (stop - i0 + kStep - 1) / kStep);
+    };
+    // Fills stage s with the tile whose boxes the lanes box_tile * boxes .. have in `c`.
+    auto issue = [&](int s, const Box& c, int32_t box_tile) {
+      uint8_t* stage = ring + s * C::STAGE_BYTES;
+      uint8_t* extra = extras + s * C::EXTRA_BYTES;
+      const bool load = my_tile == box_tile && c.need;
+      const uint32_t have = __ballot_sync(0xffffffffu, load);
+      const int leader = box_tile * boxes;
+      const bool with_q = __shfl_sync(0xffffffffu, c.h.flags, leader) & 1;
+      if (lane == leader) {
+        sm.hdr[s] = c.h;
+        ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + (with_q ? heads * D * 2 : 0));
+      }
+      __syncwarp();
+      if (load) issue_box<C>(stage, tk, tv, my_row, c.row, c.id, &sm.full[s]);
+      if (with_q) {
+        const int64_t row = (int64_t)__shfl_sync(0xffffffffu, c.h.b, leader) * Hq + __shfl_sync(0xffffffffu, c.h.h0, leader);
+        if (lane < heads)
+          bulk_load(extra + C::SCALE_BYTES + lane * C::Q_ROW, p.q + (row + lane) * D, D * 2, &sm.full[s]);
+      }
+      if (!BF) {
+        // The tile's exponent bytes, [page][K, V][row], 16 of them a lane: a bulk copy per page would be as many
+        // copies again as the codes take where pages are small.
+        const int32_t at = lane * 16, from = leader + ((at >> (p.log2_page + 1)) << p.log2_page >> log2_box);
+        // of a page of two boxes, either may be the only one that is loaded
+        const int32_t box_at = (p.log2_page == log2_box || (have >> (from & 31) & 1) ? from : from + 1) & 31;
+        const int32_t id = __shfl_sync(0xffffffffu, c.id, box_at);
+        if (lane < C::SCALE_BYTES / 16 && (have >> box_at & 1))
+          cp_async16(extra + at, p.kv_scale + ((int64_t)id << (p.log2_page + 1)) + (at & (2 * page - 1)));
+        cp_async_arrive(&sm.full[s]);
+      }
+      __syncwarp();
+    };
+    auto check_id = [&](Box& c) {
+      if (c.need && (uint32_t)c.id >= (uint32_t)p.num_pages) {
+        report(p.status, 1);
+        c.id = 0;
+      }
     };
     // Joins the warps' results of the chunk in mail `k`: each helper those of its quarter's warps (w, w + 4, w + 8), then
     // all four together, a quarter of the columns each.
@@ -625,6 +696,28 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     uint32_t mails = 0;
     int32_t idle = 0;
     cur.need = nxt.need = false;
+    if (per == 1 && warp == C::WARPS && tiles > 0 && sm.window[0].g.n > sm.tile0) {
+      // Tile 0 straight from its pair's geometry, 0.7 us before the first batch is planned.
+      const DecodePair& w0 = sm.window[0];
+      const int32_t tile = sm.tile0;
+      const DecodeSpan sp = decode_span(w0.g, tile, p.log2_page);
+      const int64_t tok = (int64_t)sp.t0 + my_row;
+      cur.need = my_tile == 0 && tok + box > sp.lo && tok < sp.hi;
+      cur.row = (int32_t)(tok & (page - 1));
+      cur.id = 0;
+      if (cur.need) {
+        const int32_t lp = (int32_t)(tok >> p.log2_page);
+        cur.id = __ldg(p.table + w0.off + (lp < w0.n_sink ? lp : lp - w0.w0 + w0.n_sink));
+      }
+      cur.h = header(0, tile, w0.g.n, sm.pair0, w0.g.n - tile, sp, lane == 0);
+      cur.h.b = w0.b;
+      cur.h.h0 = w0.h0;
+      check_id(cur);
+      issue(0, cur, 0);
+      issued = 0;
+      i = kStep;
+      cur.need = false;
+    }
 #pragma unroll 1
     while (producing || !done) {
       if (producing && left == 0) {  // the batch that was planned last becomes the current one
@@ -636,53 +729,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         left = max(ahead, 0);
         at_box = 0;
         ahead = plan(i + left * kStep);
-        if (cur.need && (uint32_t)cur.id >= (uint32_t)p.num_pages) {
-          report(p.status, 1);
-          cur.id = 0;
-        }
+        check_id(cur);
         continue;
       }
       if (producing) {
         const int s = i % C::STAGES;
         if (i < C::STAGES || __all_sync(0xffffffffu, ptx::mbar_try_wait(&sm.empty[s], ((i / C::STAGES) - 1) & 1))) {
           idle = 0;
-          uint8_t* stage = ring + s * C::STAGE_BYTES;
-          uint8_t* extra = extras + s * C::EXTRA_BYTES;
-          const bool load = my_tile == at_box && cur.need;
-          const uint32_t have = __ballot_sync(0xffffffffu, load);
-          const int leader = at_box * boxes;
-          const bool with_q = __shfl_sync(0xffffffffu, cur.h.flags, leader) & 1;
-          if (lane == leader) {
-            sm.hdr[s] = cur.h;
-            ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + (with_q ? heads * D * 2 : 0));
-          }
+          issue(s, cur, at_box);
           issued = i;
-          __syncwarp();
-          if (with_q) {
-            const int64_t row = (int64_t)__shfl_sync(0xffffffffu, cur.h.b, leader) * Hq + __shfl_sync(0xffffffffu, cur.h.h0, leader);
-            if (lane < heads)
-              bulk_load(extra + C::SCALE_BYTES + lane * C::Q_ROW, p.q + (row + lane) * D, D * 2, &sm.full[s]);
-          }
-          if (load) {
-#pragma unroll
-            for (int cb = 0; cb < C::CB; ++cb) {
-              const int at = cb * C::BLOCK_BYTES + my_row * C::ROWB;
-              ptx::tma_load_3d(stage + at, &tk, cb * (C::ROWB / C::EB), cur.row, cur.id, &sm.full[s]);
-              ptx::tma_load_3d(stage + C::TILE_BYTES + at, &tv, cb * (C::ROWB / C::EB), cur.row, cur.id, &sm.full[s]);
-            }
-          }
-          if (!BF) {
-            // The tile's exponent bytes, [page][K, V][row], 16 of them a lane: a bulk copy per page would be as many
-            // copies again as the codes take where pages are small.
-            const int32_t at = lane * 16, from = at_box * boxes + ((at >> (p.log2_page + 1)) << p.log2_page >> log2_box);
-            // of a page of two boxes, either may be the only one that is loaded
-            const int32_t box_at = (p.log2_page == log2_box || (have >> (from & 31) & 1) ? from : from + 1) & 31;
-            const int32_t id = __shfl_sync(0xffffffffu, cur.id, box_at);
-            if (lane < C::SCALE_BYTES / 16 && (have >> box_at & 1))
-              cp_async16(extra + at, p.kv_scale + ((int64_t)id << (p.log2_page + 1)) + (at & (2 * page - 1)));
-            cp_async_arrive(&sm.full[s]);
-          }
-          __syncwarp();
           --left;
           ++at_box;
           i += kStep;
