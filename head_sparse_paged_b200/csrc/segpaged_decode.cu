@@ -43,7 +43,11 @@ int sm_count() {
   return device_sm_count(dev);
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA; }
+// The code of a CUDA call that failed, which is not left behind for the next call's check to find.
+int cuda_failed() {
+  cudaGetLastError();
+  return SEGPAGED_ERR_CUDA;
+}
 
 // A launch that may start while the work before it ends; the kernel waits for that before it reads or writes anything,
 // so that only its set-up overlaps the last blocks of what came before.
@@ -59,7 +63,7 @@ int launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SEGPAGED_OK : SEGPAGED_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? SEGPAGED_OK : cuda_failed();
 }
 
 // Blocks of the kernels that take a slice of a page a warp: a warp for each slice (the kernels loop past the limit).
@@ -113,13 +117,13 @@ int launch_decode_nb(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeP
   if (!configured[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(decode_kernel<D, FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
         cudaSuccess)
-      return SEGPAGED_ERR_CUDA;
+      return cuda_failed();
     configured[dev].store(true, std::memory_order_release);
   }
   if (launch_early(decode_kernel<D, FMT, NB>, dim3(grid), C::THREADS, C::SMEM_BYTES, st, tk, tv, p)) return SEGPAGED_ERR_CUDA;
   if (!p.whole && launch_early(decode_combine_kernel<D>, dim3(grid, std::min(p.G, kDecodeGroup)), 32 * kDecodeCombineWarps, 0, st, p))
     return SEGPAGED_ERR_CUDA;
-  return launched();
+  return SEGPAGED_OK;
 }
 
 // Up to eight query heads a KV head fill one column block of the products, up to sixteen two; larger groups take
@@ -194,7 +198,7 @@ extern "C" int segpaged_build_quant(const segpaged_dims* dims, int32_t kv_format
   p.log2_page = log2_int(dims->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   SEGPAGED_BY_SHAPE_8BIT(rc = launch_build_quant, (p, slice_blocks(page_table_len, p.log2_page), st));
-  return rc == SEGPAGED_OK ? launched() : rc;
+  return rc;
 }
 
 extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, const void* k_new, const void* v_new,
@@ -230,7 +234,7 @@ extern "C" int segpaged_append(const segpaged_dims* dims, int32_t kv_format, con
   p.num_pages = dims->num_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   SEGPAGED_BY_SHAPE(rc = launch_append, (p, st));
-  return rc == SEGPAGED_OK ? launched() : rc;
+  return rc;
 }
 
 namespace {
@@ -270,7 +274,7 @@ extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_form
   p.num_pages = dims->num_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   SEGPAGED_BY_SHAPE_8BIT(rc = launch_dequant, (p, slice_blocks(page_table_len, p.log2_page), st));
-  return rc == SEGPAGED_OK ? launched() : rc;
+  return rc;
 }
 
 // Per CTA the two chunks its run can start and end with, and which pair goes on behind it.
@@ -292,7 +296,8 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   if (!q || (!page_table && page_table_len > 0) || !page_table_offs || !ctx_len || !cls || !o || !lse || !workspace) return SEGPAGED_ERR_NULL;
   if (workspace_bytes < segpaged_decode_workspace_bytes(dims)) return SEGPAGED_ERR_CAPACITY;
   if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return SEGPAGED_ERR_ALIGN;
-  if (!std::isfinite(softmax_scale)) return SEGPAGED_ERR_DIMS;
+  const float scale_log2 = softmax_scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return SEGPAGED_ERR_DIMS;
   const int sms = sm_count();
   if (sms <= 0) return SEGPAGED_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -318,7 +323,7 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   p.num_pages = dims->num_pages;
   p.log2_hg = p.G > kDecodeGroup ? log2_int(p.G / kDecodeGroup) : 0;
   p.whole = page_table_len <= kDecodeWholeTokens >> p.log2_page;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = SEGPAGED_OK;
   SEGPAGED_BY_SHAPE(rc = launch_decode, (k_pool, v_pool, p, std::min(sms, kDecodeMaxCtas), st));

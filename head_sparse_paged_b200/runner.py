@@ -392,7 +392,8 @@ class Decoder:
         self.offs_dev[li].copy_(torch.from_numpy(offs))
 
     def advance(self):
-        """Makes room for one more token per sequence; call once before the layers' steps."""
+        """Makes room for one more token per sequence; call once before the layers' steps. It changes the lengths and tables
+        on the current stream, so steps that run on another stream have to be ordered against it by the caller."""
         if int(self.ctx[0] - self.r.ctx[0]) >= self.max_new:
             raise RuntimeError(f"the decoder was set up for {self.max_new} new tokens")
         self.ctx += 1

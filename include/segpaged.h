@@ -447,13 +447,13 @@ size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims);
  *   k_pool, v_pool, kv_scale (dev): pools of kv_format (kv_scale ignored for bf16, may be NULL). They hold the
  *     token's own key and value already (segpaged_append, segpaged_build, segpaged_build_quant). Rows the token
  *     cannot see (past L_b, outside sink and window) may hold anything, NaN included.
- *   softmax_scale: any finite value (SEGPAGED_ERR_DIMS otherwise).
+ *   softmax_scale: finite, and finite when multiplied by log2(e) in fp32 (SEGPAGED_ERR_DIMS otherwise).
  *   workspace (dev) >= segpaged_decode_workspace_bytes(dims), 16-byte aligned; its contents before the call do not
  *     matter. A call owns it while it runs: calls (or replayed graphs) that may overlap on the GPU need one each.
  *   o and lse must not overlap q or one another.
- * Logits, sums and O are accumulated in fp32. A probability is rounded to fp16 (8-bit pools) or to a sum of two bf16
- * (bf16 pools). The result does not depend on the physical page ids. Of an 8-bit pool, K rows beyond 2^90 in magnitude
- * may overflow the logits before softmax_scale brings them back.
+ * Logits (times log2(e)), sums and O are held in fp32 and have to stay within its range. A probability is rounded to
+ * fp16 (8-bit pools) or to a sum of two bf16 (bf16 pools). The result does not depend on the physical page ids. Of an
+ * 8-bit pool, K rows beyond 2^90 in magnitude may overflow the logits before softmax_scale brings them back.
  * A sequence with L_b = 0 (an unused batch slot) gets O = 0 and LSE = -infinity. Two kernels are launched, both able to
  * start while the work before them ends (programmatic dependent launches; they wait for it before touching memory).
  */

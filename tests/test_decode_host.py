@@ -128,6 +128,8 @@ def test_refusals_of_each_call():
         assert _call("segpaged_attn_decode", **{a: P8}) == ALIGN
     for bad in (float("nan"), float("inf")):
         assert _call("segpaged_attn_decode", scale=bad) == DIMS
+    for bad in (2.9e38, -2.9e38):                            # finite, but not times log2(e)
+        assert _call("segpaged_attn_decode", scale=bad) == DIMS
     assert _call("segpaged_attn_decode", ws_bytes=16) == CAPACITY and _call("segpaged_attn_decode", tlen=-1) == DIMS
     assert sp.error_string(FORMAT).startswith("a pool format")
 
