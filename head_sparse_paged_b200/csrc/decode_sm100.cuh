@@ -10,7 +10,7 @@
 //     lengths and there is no host plan. Runs that end inside a pair leave a partial result (O / l and its log2-sum) in
 //     the workspace, which decode_combine_kernel joins in tile order: no atomics, no state from call to call, and the
 //     result depends on the lengths and the grid only.
-//   - Two of four helper warps stream the tiles through a ring of shared-memory stages with TMA (page id = coordinate),
+//   - Two to four helper warps stream the tiles through a ring of shared-memory stages with TMA (page id = coordinate),
 //     three (bf16) or six (8-bit) tiles deep, across pair boundaries, with the page ids of the next tiles in flight.
 //   - Eight (bf16) or twelve (8-bit) consumer warps take 32 tokens of every second or third tile, and keep their own
 //     running maximum, sum and O in registers. S^T = K Q^T puts the tokens on the 16 rows of mma.m16n8k16 and the heads
@@ -50,7 +50,6 @@ namespace segpaged {
 
 constexpr int kDecodeTile = 128;         // tokens of a tile
 constexpr int kDecodeMaxWarps = 12;      // most consumer warps
-constexpr int kDecodeProducers = 2;      // helper warps that issue copies
 constexpr int kDecodeHelpers = 4;        // warps beside the consumers: one for each quarter of tensor memory's lanes
 constexpr int kDecodeMails = 2;          // finished chunks that tensor memory holds
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
@@ -106,10 +105,11 @@ struct DecodeCfg {
   static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
+  static constexpr int PRODUCERS = FMT == kFmtBf16 ? 2 : kDecodeHelpers;  // most helpers that issue copies
   // A producer's wait for a stage looks at one parity bit, so the stage may be at most one use behind it: what it waited
   // for before its last tile, as many tiles ago as there are producers, has to cover the use before the last one,
   // 2 STAGES tiles ago.
-  static_assert(STAGES >= 2 && STAGES <= 8 && kDecodeProducers <= STAGES, "ring");
+  static_assert(STAGES >= 2 && STAGES <= 8 && PRODUCERS <= STAGES, "ring");
   static constexpr int THREADS = 32 * (WARPS + kDecodeHelpers);
   // Tensor-memory columns of one warp's O in its quarter of the lanes, of a chunk, and of all of them.
   static constexpr int OCOLS = NB * D / 4;
@@ -434,9 +434,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 
   if (warp >= C::WARPS) {
     // ------------------------------------------------------------------------------------- helpers
-    // The first kDecodeProducers helpers issue the copies. Producer j does tiles j, j + kStep, ... of the run: preparing and
-    // issuing a tile's copies takes a warp 0.5 us (pages of 64 rows) to 0.9 us (of 16), as long as the bytes take, and is a
-    // chain of latencies that two warps overlap (pages of 16 in e4m3: 93 us with one, 67 with two, three and four).
+    // The first n_step helpers issue the copies. Producer j does tiles j, j + n_step, ... of the run: preparing and issuing a
+    // tile's copies takes a warp 0.5 us (pages of 64 rows) to 0.9 us (of 16), and is a chain of latencies that several warps
+    // overlap. Two do for the tiles of 128 columns in pages of 32 and more; half as large ones, and eight boxes to a
+    // tile, go faster with four: 32 sequences of 16-32K in e4m3 with pages of 16 take 69.1 us with two and 63.6 us with
+    // four, with 64 columns 46.1 and 45.2 us, with both 63.1 and 46.8 us. Where two do, four cost up to 1 us (64 sequences
+    // of 0.1-0.9K: 21.6 and 22.6 us): the helpers join the chunks too. bf16 tiles are twice as large and gain nothing.
     // Each works in batches of 32 boxes (a box: up to 64 rows of one page; 2 to 8 to a tile), one per lane: the lanes find
     // their boxes' pages for the next batch, whose loads are then in flight while this batch's copies are issued.
     // (Looking one tile ahead instead left 0.9 us per tile, the latency of a page id under load: 5.0 TB/s of an
@@ -445,7 +448,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     const int32_t log2_box = min(p.log2_page, 6), box = 1 << log2_box;  // rows of one TMA box
     const int32_t boxes = kDecodeTile >> log2_box, batch_tiles = 32 / boxes;
     const int32_t my_tile = lane / boxes, my_row = (lane % boxes) * box;
-    constexpr int32_t kStep = kDecodeProducers;
+    const int32_t log2_step = BF ? 1 : D == 64 || p.log2_page == 4 ? 2 : 1;
+    const int32_t n_step = 1 << log2_step;
     // Window: lane k holds pair window + k, whose tiles are [w_end - w.g.n, w_end) of this CTA's run.
     int32_t window = sm.pair0 - 32, w_end = -sm.tile0;  // the pairs before the run: to be followed by its first 32
     DecodePair w = {};
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       }
       return h;
     };
-    // The boxes of tiles i0, i0 + kStep, ... into nxt; returns how many tiles that are (0: the run is done).
+    // The boxes of tiles i0, i0 + n_step, ... into nxt; returns how many tiles that are (0: the run is done).
     auto plan = [&](int32_t i0) -> int32_t {
       nxt.need = false;
       if (i0 >= tiles) return 0;
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         stop = __shfl_sync(0xffffffffu, w_end, 31);
       }
       stop = min(stop, tiles);
-      const int32_t i = min(i0 + my_tile * kStep, stop - 1);
+      const int32_t i = min(i0 + my_tile * n_step, stop - 1);
       int32_t k = 0;  // pairs of the window that end at or before tile i
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1)
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       const int32_t tile = i - (end_k - n);
       const DecodeSpan sp = decode_span(g, tile, p.log2_page);
       const int32_t t0 = sp.t0, lo = sp.lo, hi = sp.hi;
-      const bool mine = i0 + my_tile * kStep < stop;
+      const bool mine = i0 + my_tile * n_step < stop;
       nxt.h = header(i, tile, n, window + k, end_k, sp, mine && my_row == 0);
       nxt.h.b = __shfl_sync(0xffffffffu, w.b, k);
       nxt.h.h0 = __shfl_sync(0xffffffffu, w.h0, k);
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         const int32_t lp = (int32_t)(tok >> p.log2_page);
         nxt.id = __ldg(p.table + off + (lp < sink ? lp : lp - w0 + sink));
       }
-      return min(batch_tiles, (stop - i0 + kStep - 1) / kStep);
+      return min(batch_tiles, (stop - i0 + n_step - 1) >> log2_step);
     };
     // Fills stage s with the tile whose boxes the lanes box_tile * boxes .. have in `c`.
     auto issue = [&](int s, const Box& c, int32_t box_tile) {
@@ -692,7 +696,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 
     // Both jobs in turn: a copy as soon as its stage is free, a join as soon as a chunk is in the mail.
     int32_t i = warp - C::WARPS, left = 0, at_box = 0, ahead = -1, issued = -1;  // issued: the last tile
-    bool producing = tiles > 0 && i < kStep, done = tiles == 0;
+    bool producing = tiles > 0 && i < n_step, done = tiles == 0;
     uint32_t mails = 0;
     int32_t idle = 0;
     cur.need = nxt.need = false;
@@ -715,7 +719,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       check_id(cur);
       issue(0, cur, 0);
       issued = 0;
-      i = kStep;
+      i = n_step;
       cur.need = false;
     }
 #pragma unroll 1
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         cur = nxt;
         left = max(ahead, 0);
         at_box = 0;
-        ahead = plan(i + left * kStep);
+        ahead = plan(i + left * n_step);
         check_id(cur);
         continue;
       }
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           issued = i;
           --left;
           ++at_box;
-          i += kStep;
+          i += n_step;
         }
       }
       if (!done) {
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     // after a timeout: the copies in flight land before the block's memory is given up
     if (*(volatile int32_t*)&sm.abort)
 #pragma unroll 1
-      for (int32_t k = issued; k >= 0 && k > issued - C::STAGES; k -= kStep)
+      for (int32_t k = issued; k >= 0 && k > issued - C::STAGES; k -= n_step)
         ptx::mbar_wait(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
   } else {
     // ----------------------------------------------------------------------------------- consumers
