@@ -12,7 +12,7 @@
 //     result depends on the lengths and the grid only.
 //   - Two to four helper warps stream the tiles through a ring of shared-memory stages with TMA (page id = coordinate),
 //     three (bf16) or six (8-bit) tiles deep, across pair boundaries, with the page ids of the next tiles in flight.
-//   - Eight (bf16) or twelve (8-bit) consumer warps take 32 tokens of every second or third tile, and keep their own
+//   - Eight or twelve consumer warps take 32 tokens of every second or third tile, and keep their own
 //     running maximum, sum and O in registers. S^T = K Q^T puts the tokens on the 16 rows of mma.m16n8k16 and the heads
 //     on its 8 columns, so up to 8 heads cost the same and nothing is padded from 8 to 16; O^T = V^T P^T likewise.
 //   - Where a pair ends, a consumer leaves its maxima and sums in shared memory and its O in tensor memory (0.25 us) and
@@ -82,10 +82,13 @@ template <int D, int FMT, int NB>
 struct DecodeCfg {
   // A warp takes 32 tokens of every second or third tile: two independent chains of products, and one maximum, wait and
   // header for twice the tokens. (16 tokens of every tile: 89.2 instead of 80.5 us with 16 heads on 32 sequences of
-  // 16-32K in e4m3.) Twelve consumer warps leave 128 registers a thread, too few for the O and q of 16 heads; for bf16
-  // pools, whose stages are three, a third turn would only hold one more of them (see STAGES).
+  // 16-32K in e4m3.) Twelve consumer warps leave 128 registers a thread, too few for the O and q of 16 heads of 128 columns;
+  // for bf16 pools of 128 columns, whose stages are three, a third turn would only hold one more of them (see STAGES). With
+  // 64 columns twelve warps against eight take 56.7 instead of 59.2 us on the same sequences with 16 heads in e4m3, and 17.9
+  // instead of 19.7 us on 64 of 0.1-0.9K with 4 heads in bf16; with 16 heads in bf16 66.5 instead of 64.3 us.
   static constexpr int MB = 2;
-  static constexpr int WARPS = NB == 1 && FMT != kFmtBf16 ? 12 : 8;               // consumer warps
+  static constexpr bool BYTES = FMT != kFmtBf16;
+  static constexpr int WARPS = (NB == 1 ? BYTES || D == 64 : BYTES && D == 64) ? 12 : 8;  // consumer warps
   static constexpr int TILE_WARPS = kDecodeTile / (16 * MB);     // of which these share a tile
   static constexpr int TURNS = WARPS / TILE_WARPS;
   static constexpr int EB = FMT == kFmtBf16 ? 2 : 1;             // bytes of an element
@@ -101,7 +104,7 @@ struct DecodeCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int EXTRA_BYTES = SCALE_BYTES + Q_BYTES;      // beside a stage: exponent bytes, query rows
   static constexpr int MERGE_BYTES = kDecodeHelpers * 8 * D * 4;  // a helper's sum of one column block of O
-  static constexpr int FIXED_BYTES = MERGE_BYTES + 3840 + 1024;  // + barriers and small arrays, alignment slack
+  static constexpr int FIXED_BYTES = MERGE_BYTES + (D == 64 ? 4864 : 3840) + 1024;  // + DecodeSmall, alignment slack
   static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
@@ -110,13 +113,15 @@ struct DecodeCfg {
   // for before its last tile, as many tiles ago as there are producers, has to cover the use before the last one,
   // 2 STAGES tiles ago.
   static_assert(STAGES >= 2 && STAGES <= 8 && PRODUCERS <= STAGES, "ring");
+  static constexpr int MAIL = WARPS * 8 * NB <= 128 ? 128 : 192;  // entries of a mail's arrays
   static constexpr int THREADS = 32 * (WARPS + kDecodeHelpers);
   // Tensor-memory columns of one warp's O in its quarter of the lanes, of a chunk, and of all of them.
   static constexpr int OCOLS = NB * D / 4;
   static constexpr int MAIL_COLS = (WARPS + 3) / 4 * OCOLS;
   static constexpr int TMEM_COLS = kDecodeMails * MAIL_COLS <= 64 ? 64 : kDecodeMails * MAIL_COLS <= 128 ? 128 : 256;
   static_assert(kDecodeMails * MAIL_COLS <= TMEM_COLS, "tensor memory");
-  static_assert(WARPS * 8 * NB <= 128 && WARPS % 4 == 0 && WARPS <= kDecodeMaxWarps, "a mail's arrays, the quarters");
+  static_assert(WARPS * 8 * NB <= MAIL && WARPS % 4 == 0 && WARPS <= kDecodeMaxWarps, "a mail's arrays, the quarters");
+  static_assert(MAIL == 128 || D == 64, "FIXED_BYTES");
   // What ending a pair costs a CTA, in half tiles of 128 columns. Of 3, 5, 7 and 9 for 8-bit pools 32 sequences of 16-32K
   // took 65.3, 63.4, 62.8 and 62.9 us and 64 of 0.1-0.9K 23.9, 22.8, 22.9 and 23.1 us; of 1, 2, 4 and 6 for bf16 108.8,
   // 107.0, 106.9, 107.4 us and 30.5, 25.6, 24.5, 24.7 us.
@@ -286,19 +291,21 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 
 // A finished chunk as the consumers leave it for the helpers: each warp's maxima (log2 units), sums and unit of O, which
 // lies in tensor memory.
+template <int N>
 struct DecodeMail {
-  float m[128], l[128];             // [consumer warp][8 NB heads]: 12 x 8 or 8 x 16 of them
+  float m[N], l[N];                 // [consumer warp][8 NB heads]
   int32_t vref[kDecodeMaxWarps];    // the exponent byte r + 127 of the unit 2^(r - 14) of its O
   int32_t b, h0, slot, final;  // first sequence and head, partial slot or -1, whether it is the run's last chunk
 };
 
 // Shared memory beside the ring and the helpers' sums.
+template <int N>
 struct DecodeSmall {
   uint64_t full[8], empty[8];
   uint64_t mail_full[kDecodeMails], mail_empty[kDecodeMails];
   uint64_t sync;                                // the helpers' meeting point
   DecodeTileHeader hdr[8];
-  DecodeMail mail[kDecodeMails];
+  DecodeMail<N> mail[kDecodeMails];
   int32_t warp_sum[kDecodeMaxWarps + kDecodeHelpers];
   int32_t first_rank, end_rank;                 // this CTA's run in the list of all tiles
   int32_t pair0, tile0;                         // where its first tile lies
@@ -306,7 +313,7 @@ struct DecodeSmall {
   uint32_t tmem;
   DecodePair window[32];                        // pairs pair0 ..
 };
-static_assert(sizeof(DecodeSmall) <= 3840, "small shared arrays");
+static_assert(sizeof(DecodeSmall<192>) <= 4864 && sizeof(DecodeSmall<128>) <= 3840, "small shared arrays");
 
 template <int D, int FMT, int NB>
 __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* extras = ring + C::STAGES * C::STAGE_BYTES;
   float4* merge = reinterpret_cast<float4*>(extras + C::STAGES * C::EXTRA_BYTES);  // [helper][KS][lane]
-  DecodeSmall& sm = *reinterpret_cast<DecodeSmall*>(extras + C::STAGES * C::EXTRA_BYTES + C::MERGE_BYTES);
+  DecodeSmall<C::MAIL>& sm = *reinterpret_cast<DecodeSmall<C::MAIL>*>(extras + C::STAGES * C::EXTRA_BYTES + C::MERGE_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t cta = blockIdx.x;
   const int32_t pairs = (p.B * p.Hkv) << p.log2_hg;
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     constexpr int KS = D / 16, OC = D / 4;
     const int g = lane >> 2, t = lane & 3, quarter = warp & 3;
     auto join = [&](int k) {
-      const DecodeMail& mail = sm.mail[k];
+      const auto& mail = sm.mail[k];
       ptx::tc_fence_after();
       const int32_t b = mail.b, h0 = mail.h0, slot = mail.slot;
       // The largest unit of the warps' O. It is applied to the finished quotients: as part of a weight it would take
@@ -1055,7 +1062,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       if (mails >= kDecodeMails && !warp_wait(&sm.mail_empty[k], (mails / kDecodeMails - 1) & 1, &sm.abort, p.status)) break;
       ++mails;
       ptx::tc_fence_after();
-      DecodeMail& mail = sm.mail[k];
+      auto& mail = sm.mail[k];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
