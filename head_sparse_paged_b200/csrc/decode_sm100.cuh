@@ -6,7 +6,7 @@
 // flops per bf16 byte, where mma.sync passes about 60). What matters is that all SMs load all the time. So:
 //   - The work is the list of 128-token tiles of all (sequence, KV head) pairs, cut into one equal run of tiles per
 //     CTA (one CTA per SM): a pair's tiles may end in one CTA and go on in the next. Each CTA finds its run by itself
-//     from ctx_len and the classes in device memory (a prefix sum over the pairs, 1.5 us), so a captured call follows the
+//     from ctx_len and the classes in device memory (a prefix sum over the pairs, 1.5-2 us), so a captured call follows the
 //     lengths and there is no host plan. Runs that end inside a pair leave a partial result (O / l and its log2-sum) in
 //     the workspace, which decode_combine_kernel joins in tile order: no atomics, no state from call to call, and the
 //     result depends on the lengths and the grid only.
@@ -30,12 +30,12 @@
 // costs a second V product where the tensor pipe idles.
 //
 // Measured (B200, back-to-back calls; of the 6543 GB/s that a large copy reaches): 32 sequences of 16-32K, 64/8 heads,
-// one global head each: bf16 106.9 us, 6.1 TB/s (94 %); e4m3 63.3 us, 5.2 TB/s (80 %); int8 65.9 us. 64 global heads at
-// 128K: bf16 612 us, 7.0 TB/s (107 %); e4m3 322 us, 6.7 TB/s (103 %), 344 us after seconds of it, when the power cap
+// one global head each: bf16 106.4 us, 6.2 TB/s (94 %); e4m3 62.0 us, 5.3 TB/s (82 %); int8 64.2 us. 64 global heads at
+// 128K: bf16 614 us, 7.0 TB/s (107 %); e4m3 321 us, 6.7 TB/s (103 %), 337 us after seconds of it, when the power cap
 // holds the SMs at 1.6 GHz and the conversions' ALU work (53 % of its pipe at 1.9 GHz) no longer hides. What the short
-// calls are made of, on 32 sequences in e4m3: 2.6 us to find the run, 2.3 us to the first copy, 2.3 us to the first tile, 47 us
-// of tiles, 2 us to the last chunk's results, 1.2 us to the combine kernel's start, 2.6 us in it, and 4 us between the
-// mean and the last CTA.
+// calls are made of, on 32 sequences in e4m3: 2.6 us to find the run, 1.2 us to issue the first copies, 1.4 us to the first
+// tile, 48 us of tiles, 2 us to the last chunk's results, 1.3 us to the combine kernel's start, 2.6 us in it, and 4 us
+// between the median and the last CTA.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
