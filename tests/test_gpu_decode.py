@@ -201,6 +201,17 @@ def test_decode_matches_oracle_with_nan_in_every_hidden_row(name, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,P,G", [(64, 16, 4), (64, 64, 16), (128, 16, 8)])
+def test_decode_long_runs(D, P, G, fmt):
+    """Over 2400 tiles of 128 tokens: each of 148 blocks fills its ring of stages at least twice."""
+    ly = Layer([(9777, 1), (9504, 1), (9601, 1), (9473, 1)], 8 * G, 8, D, P, [[GLOBAL] * 7 + [local(33, 9000)]] * 4, fmt, seed=61)
+    t = ly.upload()
+    o, lse = ly.decode(t)
+    assert int(t["status"].item()) == 0
+    check_attention(o, lse, ly.attention(1.0 / math.sqrt(D)), f"{D} {P} {G} {fmt}")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("k_scale,v_scale,scale", [(8.0, 1.0, 0.5), (1e-3, 1e3, 1.0), (2.0 ** 20, 2.0 ** -60, 2.0 ** -22),
                                                    (2.0 ** -40, 2.0 ** 60, 2.0 ** 37), (1.0, 1.0, 0.0), (1.0, 1.0, -0.3),
                                                    (1.0, 2.0 ** -114, 0.1), (1.0, 2.0 ** 122, 0.1), (100.0, 1.0, 0.09)])
