@@ -7,7 +7,7 @@
 //   - The work is the list of 128-token tiles of all (sequence, KV head) pairs, cut into one equal run of tiles per
 //     CTA (one CTA per SM): a pair's tiles may end in one CTA and go on in the next. Each CTA finds its run by itself
 //     from ctx_len and the classes in device memory (a prefix sum over the pairs, 1.5-2 us), so a captured call follows the
-//     lengths and there is no host plan. Runs that end inside a pair leave a partial result (O / l and its log2-sum) in
+//     lengths and there is no host plan. Runs that end inside a pair leave a partial result (O / l, m and l) in
 //     the workspace, which decode_combine_kernel joins in tile order: no atomics, no state from call to call, and the
 //     result depends on the lengths and the grid only.
 //   - Two to four helper warps stream the tiles through a ring of shared-memory stages with TMA (page id = coordinate),
@@ -54,7 +54,6 @@ constexpr int kDecodeHelpers = 4;        // warps beside the consumers: one for 
 constexpr int kDecodeMails = 2;          // finished chunks that tensor memory holds
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
-constexpr float kDecodeMinScale = 0x1p-120f;  // in place of a logit scale of 0: 0 x -infinity is not wanted
 constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
 
 struct DecodeParams {
@@ -68,7 +67,7 @@ struct DecodeParams {
   __nv_bfloat16* o;            // [B][Hq][D]
   float* lse;                  // [Hq][B]
   float* part_o;               // [2 x CTAs][16][D]: O / l of a chunk
-  float* part_lse;             // [2 x CTAs][16]: its log2 sum
+  float2* part_sum;            // [2 x CTAs][16]: its maximum m (log2 units) and sum l
   int32_t* part_meta;          // [CTAs][2]: pair and chunk count of the pair whose first chunk is this CTA's last
   int32_t* status;             // nullable
   int64_t table_len;
@@ -690,9 +689,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             for (int j = 0; j < 2; ++j) {
               const int head = nb * 8 + 2 * t + j;
               if (head >= heads) continue;
-              const float lse2 = top[j] + log2f(sum[j]);
-              if (slot < 0) p.lse[(int64_t)(h0 + head) * p.B + b] = 0.6931471805599453f * lse2;
-              else p.part_lse[(int64_t)slot * kDecodeGroup + head] = lse2;
+              if (slot < 0) p.lse[(int64_t)(h0 + head) * p.B + b] = 0.6931471805599453f * (top[j] + log2f(sum[j]));
+              else p.part_sum[(int64_t)slot * kDecodeGroup + head] = make_float2(top[j], sum[j]);
             }
         }
         if (!meet()) return false;  // `merge` is free again
@@ -801,9 +799,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       return (base ^ ((c & 7) << 4)) + (c >> 3) * C::BLOCK_BYTES + mb * 16 * C::ROWB;
     };
     uint32_t qf[NB][KS][2];
-    // Logits are kept as y = (+-q') . k' with the K row's exponent in, which f = head_scale > 0 takes to log2 units: the
-    // maximum m is one of y, and a probability 2^(f y - f m) is one fma and one ex2.
-    float head_scale[NB][2];                     // of heads 2t, 2t + 1
+    // Logits y are kept in log2 units, rounded to fp32 once, and a probability is 2^(y - m): at most 1, and 1 at the
+    // maximum, whatever the size of y. (A product with the scale and the subtraction as one fma would be off by the
+    // rounding of the scaled maximum, a factor of 2 or more from logits of 2^25 on: past the range of fp16, then of fp32.)
+    float head_scale[NB][2];                     // of heads 2t, 2t + 1: what takes q' . k' to y but for the K row's exponent
     float m[NB][2], l[NB][2], o[NB][KS][4];
     int32_t vref = 0;                            // r + 127
     uint32_t mails = 0;
@@ -833,24 +832,23 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
               // fp16: the contraction runs in the order the code bytes lie in, 4t .. 4t+3 of each 16
               const int d = 16 * ks + (BF ? 2 * t + 8 * j : 4 * t + 2 * j);
               qf[nb][ks][j] = head < heads ? *reinterpret_cast<const uint32_t*>(qs + head * C::Q_ROW + 2 * d) : 0u;
-              if (BF) qf[nb][ks][j] ^= p.scale_log2 < 0.f ? 0x80008000u : 0u;
               top = absmax2(top, qf[nb][ks][j]);
             }
           }
           if (BF) {
-            head_scale[nb][0] = head_scale[nb][1] = fmaxf(fabsf(p.scale_log2), kDecodeMinScale);
+            head_scale[nb][0] = head_scale[nb][1] = p.scale_log2;
           } else {
             top = max2(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max2(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int32_t biased = (int32_t)(max(top & 0xffffu, top >> 16) >> 7);
             const int32_t e = biased == 255 ? 0 : 15 - max(biased - 127, -100);  // not finite: as it is
-            const float up = copysignf(exp2_int(e), p.scale_log2);
+            const float up = exp2_int(e);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 qf[nb][ks][j] = pack_f16x2(bf16_lo(qf[nb][ks][j]) * up, bf16_hi(qf[nb][ks][j]) * up);
-            const float back = fmaxf(fabsf(p.scale_log2) * exp2_int(-e), kDecodeMinScale);
+            const float back = p.scale_log2 * exp2_int(-e);
             head_scale[nb][0] = __shfl_sync(0xffffffffu, back, 8 * t);
             head_scale[nb][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
           }
@@ -941,6 +939,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             for (int j = 0; j < 2; ++j) {
               float& x0 = sc[mb][nb][2 * j];
               float& x1 = sc[mb][nb][2 * j + 1];
+              x0 *= f0;  // before the K row's exponent: a scale that makes up for large keys does so in time
+              x1 *= f1;
               if (!BF) {
                 x0 *= kscale[mb][j];
                 x1 *= kscale[mb][j];
@@ -961,9 +961,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           n1 = fmaxf(n1, m[nb][1]);
           // a larger maximum (or V exponent) rescales what was summed so far
           if (__any_sync(0xffffffffu, n0 != m[nb][0] || n1 != m[nb][1] || vshift != 1.f)) {
-            // (the difference of the rounded f m that the probabilities are relative to, not f times the difference)
-            const float c0 = m[nb][0] == -INFINITY ? 0.f : ptx::ex2(__fmul_rn(f0, m[nb][0]) - __fmul_rn(f0, n0));
-            const float c1 = m[nb][1] == -INFINITY ? 0.f : ptx::ex2(__fmul_rn(f1, m[nb][1]) - __fmul_rn(f1, n1));
+            const float c0 = m[nb][0] == -INFINITY ? 0.f : ptx::ex2(m[nb][0] - n0);
+            const float c1 = m[nb][1] == -INFINITY ? 0.f : ptx::ex2(m[nb][1] - n1);
             // NaN sums stay NaN: 0 * NaN
             l[nb][0] *= c0;
             l[nb][1] *= c1;
@@ -978,12 +977,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
             m[nb][0] = n0;
             m[nb][1] = n1;
           }
-          const float b0 = n0 == -INFINITY ? 0.f : -__fmul_rn(f0, n0), b1 = n1 == -INFINITY ? 0.f : -__fmul_rn(f1, n1);
+          const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float p0 = ptx::ex2(fmaf(sc[mb][nb][2 * j], f0, b0)), p1 = ptx::ex2(fmaf(sc[mb][nb][2 * j + 1], f1, b1));
+              const float p0 = ptx::ex2(sc[mb][nb][2 * j] - b0), p1 = ptx::ex2(sc[mb][nb][2 * j + 1] - b1);
               l[nb][0] += p0;
               l[nb][1] += p1;
               if (BF) {
@@ -1070,7 +1069,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], d);
           if (g == 0) {
-            mail.m[(warp * NB + nb) * 8 + 2 * t + j] = m[nb][j] == -INFINITY ? m[nb][j] : __fmul_rn(head_scale[nb][j], m[nb][j]);
+            mail.m[(warp * NB + nb) * 8 + 2 * t + j] = m[nb][j];
             mail.l[(warp * NB + nb) * 8 + 2 * t + j] = l[nb][j];
           }
         }
@@ -1100,7 +1099,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   }
 }
 
-// Joins the chunks of the pairs that several CTAs shared: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
+// Joins the chunks of the pairs that several CTAs shared: with w_c = 2^(m_c - m) l_c, m the largest m_c, O is the mean of the
+// O_c weighted by w_c and LSE = ln 2 (m + log2 sum_c w_c). (A chunk's m + log2 l as one float would lose its l to rounding
+// where m is large.)
 // CTA c's last pair, if it goes on behind it, has n chunks: CTA c's second slot and the first slots of the n - 1 CTAs
 // after it. Block (c, head) joins them: each of its eight warps takes every eighth chunk, a lane D/32 columns, and the
 // warps' sums are added in order. The loads of five chunks a warp are in flight together with those of all the log
@@ -1110,7 +1111,7 @@ constexpr int kDecodeCombineWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kDecodeCombineWarps, 5) decode_combine_kernel(const DecodeParams p) {
   constexpr int E = D / 32, NW = kDecodeCombineWarps, U = 5;
-  __shared__ float s_lse[kDecodeMaxCtas], s_sum[NW], s_top[NW], s_o[NW][D];
+  __shared__ float s_m[kDecodeMaxCtas], s_l[kDecodeMaxCtas], s_sum[NW], s_top[NW], s_o[NW][D];
   const int32_t cta = blockIdx.x, head = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   early_start();  // the partial results of the launch before this one
@@ -1132,9 +1133,10 @@ __global__ void __launch_bounds__(32 * kDecodeCombineWarps, 5) decode_combine_ke
   load(warp);  // on its way while the weights are worked out
   float top = -INFINITY;
   for (int32_t c = threadIdx.x; c < n; c += 32 * NW) {
-    const float x = p.part_lse[slot(c)];
-    s_lse[c] = x;
-    top = fmaxf(top, x);
+    const float2 x = p.part_sum[slot(c)];
+    s_m[c] = x.x;
+    s_l[c] = x.y;
+    top = fmaxf(top, x.x);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -1149,7 +1151,7 @@ __global__ void __launch_bounds__(32 * kDecodeCombineWarps, 5) decode_combine_ke
     for (int u = 0; u < U; ++u) {
       const int32_t c = c0 + u * NW;
       if (c >= n) continue;
-      const float w = s_lse[c] == -INFINITY ? 0.f : ptx::ex2(s_lse[c] - top);
+      const float w = (s_m[c] == -INFINITY ? 0.f : ptx::ex2(s_m[c] - top)) * s_l[c];
       sum += w;
 #pragma unroll
       for (int k = 0; k < E; ++k) o[k] += w == 0.f ? 0.f : w * v[u][k];

@@ -280,7 +280,7 @@ extern "C" int segpaged_pages_dequant(const segpaged_dims* dims, int32_t kv_form
 // Per CTA the two chunks its run can start and end with, and which pair goes on behind it.
 extern "C" size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims) {
   const size_t D = dims && dims->head_dim == 64 ? 64 : 128;
-  return align256(kMetaBytes) + align256(kSlots * kDecodeGroup * sizeof(float)) + kSlots * kDecodeGroup * D * sizeof(float);
+  return align256(kMetaBytes) + align256(kSlots * kDecodeGroup * sizeof(float2)) + kSlots * kDecodeGroup * D * sizeof(float);
 }
 
 extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format, const void* q, const void* k_pool,
@@ -304,8 +304,8 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   DecodeParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.part_meta = reinterpret_cast<int32_t*>(ws);
-  p.part_lse = reinterpret_cast<float*>(ws + align256(kMetaBytes));
-  p.part_o = reinterpret_cast<float*>(ws + align256(kMetaBytes) + align256(kSlots * kDecodeGroup * sizeof(float)));
+  p.part_sum = reinterpret_cast<float2*>(ws + align256(kMetaBytes));
+  p.part_o = reinterpret_cast<float*>(ws + align256(kMetaBytes) + align256(kSlots * kDecodeGroup * sizeof(float2)));
   p.kv_scale = kv_scale;
   p.table = page_table;
   p.offs = page_table_offs;

@@ -451,9 +451,9 @@ size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims);
  *   workspace (dev) >= segpaged_decode_workspace_bytes(dims), 16-byte aligned; its contents before the call do not
  *     matter. A call owns it while it runs: calls (or replayed graphs) that may overlap on the GPU need one each.
  *   o and lse must not overlap q or one another.
- * Logits (times log2(e)), sums and O are held in fp32 and have to stay within its range. A probability is rounded to
- * fp16 (8-bit pools) or to a sum of two bf16 (bf16 pools). The result does not depend on the physical page ids. Of an
- * 8-bit pool, K rows beyond 2^90 in magnitude may overflow the logits before softmax_scale brings them back.
+ * Logits (times log2(e), rounded to fp32 once), sums and O are held in fp32 and have to stay within its range; of a bf16
+ * pool q.k has to as well, of an 8-bit pool a query row times softmax_scale has to stay below 2^110. A probability is
+ * rounded to fp16 (8-bit pools) or to a sum of two bf16 (bf16 pools). The result does not depend on the physical page ids.
  * A sequence with L_b = 0 (an unused batch slot) gets O = 0 and LSE = -infinity. Two kernels are launched, both able to
  * start while the work before them ends (programmatic dependent launches; they wait for it before touching memory).
  */
