@@ -26,7 +26,12 @@
 // of two first, so that bf16 queries of any size are exact in fp16 to 2^-29 of the row's largest. The K row's exponent
 // scales the logit; the V row's exponent 2^(y - r), r the largest one so far in this warp, multiplies the
 // probability, and O is kept in units of 2^(r - 14): the product, at most 2^14, is rounded to fp16 (2^-11 relative
-// down to 2^-28 of the largest). bf16 pools: a probability is split into a sum of two bf16 (2^-16 relative), which
+// down to 2^-14, 2^-25 below). While the y of a chunk lie within kDecodeSpread of one another, its most probable key weighs
+// 2^3 or more, so that nothing above 2^-28 of a head's largest weight is lost. A chunk whose y lie farther apart (a large V
+// row, maybe of no probability at all, beside small ones) is done again in fp32 behind the loop: 32 sequences of 16-32K
+// whose chunks are all like that take 927 instead of 62 us. (Units by each head's largest weight instead, in the loop: 88
+// instead of 78 us for 16 heads on such sequences in e4m3, by the registers they take, needed or not.)
+// bf16 pools: a probability is split into a sum of two bf16 (2^-16 relative), which
 // costs a second V product where the tensor pipe idles.
 //
 // Measured (B200, back-to-back calls; of the 6543 GB/s that a large copy reaches): 32 sequences of 16-32K, 64/8 heads,
@@ -55,10 +60,13 @@ constexpr int kDecodeMails = 2;          // finished chunks that tensor memory h
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
 constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
+constexpr int kDecodeSpread = 11;        // how far apart the exponent bytes of a chunk's V rows may lie in fp16 weights
 
 struct DecodeParams {
   const __nv_bfloat16* q;      // [B][Hq][D]
   const uint8_t* kv_scale;     // [num_pages][2][P], null for bf16
+  const uint8_t* k_pool;       // what the tensor maps stand for, for the 8-bit chunks that are done again
+  const uint8_t* v_pool;
   const int32_t* table;
   const int32_t* offs;         // [B*Hkv+1]
   const int32_t* ctx_len;      // [B]
@@ -103,7 +111,9 @@ struct DecodeCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int EXTRA_BYTES = SCALE_BYTES + Q_BYTES;      // beside a stage: exponent bytes, query rows
   static constexpr int MERGE_BYTES = kDecodeHelpers * 8 * D * 4;  // a helper's sum of one column block of O
-  static constexpr int FIXED_BYTES = MERGE_BYTES + (D == 64 ? 4864 : 3840) + 1024;  // + DecodeSmall, alignment slack
+  static constexpr int MAIL = WARPS * 8 * NB;                     // entries of a mail's arrays
+  static constexpr int SMALL_BYTES = MAIL <= 96 ? 3584 : MAIL <= 128 ? 3904 : 4928;  // a DecodeSmall<MAIL>
+  static constexpr int FIXED_BYTES = MERGE_BYTES + SMALL_BYTES + 1024;  // 1024: alignment slack
   static constexpr int FIT = (227 * 1024 - FIXED_BYTES) / (STAGE_BYTES + EXTRA_BYTES);
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * (STAGE_BYTES + EXTRA_BYTES);
@@ -112,15 +122,13 @@ struct DecodeCfg {
   // for before its last tile, as many tiles ago as there are producers, has to cover the use before the last one,
   // 2 STAGES tiles ago.
   static_assert(STAGES >= 2 && STAGES <= 8 && PRODUCERS <= STAGES, "ring");
-  static constexpr int MAIL = WARPS * 8 * NB <= 128 ? 128 : 192;  // entries of a mail's arrays
   static constexpr int THREADS = 32 * (WARPS + kDecodeHelpers);
   // Tensor-memory columns of one warp's O in its quarter of the lanes, of a chunk, and of all of them.
   static constexpr int OCOLS = NB * D / 4;
   static constexpr int MAIL_COLS = (WARPS + 3) / 4 * OCOLS;
   static constexpr int TMEM_COLS = kDecodeMails * MAIL_COLS <= 64 ? 64 : kDecodeMails * MAIL_COLS <= 128 ? 128 : 256;
   static_assert(kDecodeMails * MAIL_COLS <= TMEM_COLS, "tensor memory");
-  static_assert(WARPS * 8 * NB <= MAIL && WARPS % 4 == 0 && WARPS <= kDecodeMaxWarps, "a mail's arrays, the quarters");
-  static_assert(MAIL == 128 || D == 64, "FIXED_BYTES");
+  static_assert(MAIL <= 192 && WARPS % 4 == 0 && WARPS <= kDecodeMaxWarps, "a mail's arrays, the quarters");
   // What ending a pair costs a CTA, in half tiles of 128 columns. Of 3, 5, 7 and 9 for 8-bit pools 32 sequences of 16-32K
   // took 65.3, 63.4, 62.8 and 62.9 us and 64 of 0.1-0.9K 23.9, 22.8, 22.9 and 23.1 us; of 1, 2, 4 and 6 for bf16 108.8,
   // 107.0, 106.9, 107.4 us and 30.5, 25.6, 24.5, 24.7 us.
@@ -293,7 +301,9 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 template <int N>
 struct DecodeMail {
   float m[N], l[N];                 // [consumer warp][8 NB heads]
-  int32_t vref[kDecodeMaxWarps];    // the exponent byte r + 127 of the unit 2^(r - 14) of its O
+  // 8-bit pools: the largest exponent byte of the V rows it saw, which is r + 127 of the unit 2^(r - 14) of its O, and << 8
+  // the smallest (0 and 255 if it saw none).
+  int32_t vref[kDecodeMaxWarps];
   int32_t b, h0, slot, final;  // first sequence and head, partial slot or -1, whether it is the run's last chunk
 };
 
@@ -310,13 +320,167 @@ struct DecodeSmall {
   int32_t pair0, tile0;                         // where its first tile lies
   int32_t abort;
   uint32_t tmem;
+  uint32_t redo;                                // bit c: chunk c of the run is to be done again (31: and those after it)
   DecodePair window[32];                        // pairs pair0 ..
 };
-static_assert(sizeof(DecodeSmall<192>) <= 4864 && sizeof(DecodeSmall<128>) <= 3840, "small shared arrays");
+static_assert(sizeof(DecodeSmall<192>) <= 4928 && sizeof(DecodeSmall<128>) <= 3904 && sizeof(DecodeSmall<96>) <= 3584,
+              "small shared arrays");
+
+// Does the run's chunks named in `redo` again, in fp32 throughout, and replaces what was written for them. For chunks of 8-bit
+// pools whose V rows are of too different size for weights in fp16. Called by the whole block, with the ring as `scratch`.
+// Four heads at a time; a warp takes batches of 32 tokens, a lane one token's logits, then D / 32 columns of all values.
+// (Out of line, behind the loop: inlined it made every other call 1 to 6 % slower.)
+constexpr int kRedoHeads = 4;
+template <int D>
+__host__ __device__ constexpr int redo_scratch(int warps) {  // floats: queries [4][D], weights [warp][32][4], results [4][warp][D + 2]
+  return kRedoHeads * (D + warps * (32 + D + 2));
+}
+template <int D, int FMT>
+__device__ __noinline__ void decode_redo(const DecodeParams& p, float* scratch, int32_t u, int32_t tile0, int32_t tiles,
+                                         uint32_t redo, int32_t warps) {
+  constexpr int E = D / 32, H = kRedoHeads;  // columns of a lane: lane * E ..
+  constexpr float kSmall = 0x1p-20f;         // O is summed in units of 2^20: many values near the largest float
+  const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int32_t heads = min(p.G, kDecodeGroup), Hq = p.Hkv * p.G, page = 1 << p.log2_page;
+  const int32_t pairs = (p.B * p.Hkv) << p.log2_hg;
+  float* qs = scratch;
+  float4* weights = reinterpret_cast<float4*>(scratch + H * D + warp * 32 * H);
+  float* parts = scratch + H * (D + warps * 32);
+  uint32_t chunk = 0;
+#pragma unroll 1
+  for (; tiles > 0 && u < pairs; ++u, tile0 = 0) {
+    const DecodePair w = decode_pair(p, u);
+    const int32_t end = min(w.g.n, tile0 + tiles);
+    if (end <= tile0) continue;
+    tiles -= end - tile0;
+    if (!(redo >> min(chunk++, 31u) & 1)) continue;
+    const int32_t slot = tile0 == 0 && end == w.g.n ? -1 : 2 * cta + (tile0 == 0 ? 1 : 0);
+#pragma unroll 1
+    for (int32_t h0 = 0; h0 < heads; h0 += H) {
+      const int64_t q0 = ((int64_t)w.b * Hq + w.h0 + h0) * D;
+      for (int32_t x = threadIdx.x; x < H * D; x += 32 * warps)
+        qs[x] = h0 + x / D < heads ? p.scale_log2 * __bfloat162float(p.q[q0 + x]) : 0.f;
+      __syncthreads();
+      float o[H][E] = {}, m[H], l[H] = {};
+#pragma unroll
+      for (int h = 0; h < H; ++h) m[h] = -INFINITY;
+#pragma unroll 1
+      for (int32_t x = warp; x < 4 * (end - tile0); x += warps) {
+        const DecodeSpan sp = decode_span(w.g, tile0 + x / 4, p.log2_page);
+        const int64_t tok = (int64_t)sp.t0 + x % 4 * 32 + lane;
+        const bool in = tok >= sp.lo && tok < sp.hi;
+        const uint32_t ins = __ballot_sync(0xffffffffu, in);
+        if (ins == 0) continue;
+        int64_t row = 0;
+        float s[H] = {}, k_scale = 0.f, v_scale = 0.f;
+        if (in) {
+          const int32_t lp = (int32_t)(tok >> p.log2_page), at = (int32_t)tok & (page - 1);
+          int32_t id = p.table[w.off + (lp < w.n_sink ? lp : lp - w.w0 + w.n_sink)];
+          if ((uint32_t)id >= (uint32_t)p.num_pages) id = 0;  // (reported when it was loaded)
+          row = ((int64_t)id << p.log2_page) + at;
+          const uint8_t* y = p.kv_scale + ((int64_t)id << (p.log2_page + 1)) + at;
+          k_scale = row_scale(y[0]);
+          v_scale = row_scale(y[page]) * kSmall;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            const uint4 codes = *reinterpret_cast<const uint4*>(p.k_pool + row * D + c);
+            const uint32_t in4[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t c2[2];
+              codes_to_half2x2<FMT, false>(in4[i], c2[0], c2[1]);
+              const float2 k01 = __half22float2(*reinterpret_cast<const __half2*>(&c2[0]));
+              const float2 k23 = __half22float2(*reinterpret_cast<const __half2*>(&c2[1]));
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                const float4 q = *reinterpret_cast<const float4*>(qs + h * D + c + 4 * i);
+                s[h] = fmaf(q.x, k01.x, fmaf(q.y, k01.y, fmaf(q.z, k23.x, fmaf(q.w, k23.y, s[h]))));
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const float y = in ? s[h] * k_scale : -INFINITY;
+          float top = y;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          top = fmaxf(top, m[h]);
+          const float from = top == -INFINITY ? 0.f : top;
+          const float c = m[h] == -INFINITY ? 0.f : ptx::ex2(m[h] - from), e = ptx::ex2(y - from);
+          l[h] = l[h] * c + e;
+          m[h] = top;
+#pragma unroll
+          for (int i = 0; i < E; ++i) o[h][i] *= c;
+          s[h] = e * v_scale;
+        }
+        weights[lane] = make_float4(s[0], s[1], s[2], s[3]);
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 32; ++i) {
+          const int64_t from = __shfl_sync(0xffffffffu, row, i);
+          if (!(ins >> i & 1)) continue;
+          const uint8_t* at = p.v_pool + from * D + lane * E;
+          uint32_t codes, c2[2];
+          if (E == 4) codes = *reinterpret_cast<const uint32_t*>(at);
+          else codes = *reinterpret_cast<const uint16_t*>(at);
+          codes_to_half2x2<FMT, false>(codes, c2[0], c2[1]);
+          const float4 w4 = weights[i];
+          const float ws[H] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            const float v = __half2float(reinterpret_cast<const __half*>(c2)[k]);
+#pragma unroll
+            for (int h = 0; h < H; ++h) o[h][k] = fmaf(ws[h], v, o[h][k]);
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float* mine = parts + (h * warps + warp) * (D + 2);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+#pragma unroll
+        for (int i = 0; i < E; ++i) mine[lane * E + i] = o[h][i];
+        if (lane == 0) {
+          mine[D] = m[h];
+          mine[D + 1] = l[h];
+        }
+      }
+      __syncthreads();
+      const int32_t head = w.h0 + h0 + warp, own = h0 + warp;  // of the model, of this pass's group
+      if (warp < H && own < heads) {
+        const float* from = parts + warp * warps * (D + 2);
+        float top = -INFINITY, sum = 0.f, acc[E] = {};
+#pragma unroll 1
+        for (int32_t x = 0; x < warps; ++x) top = fmaxf(top, from[x * (D + 2) + D]);
+#pragma unroll 1
+        for (int32_t x = 0; x < warps; ++x) {
+          const float mx = from[x * (D + 2) + D], c = mx == -INFINITY ? 0.f : ptx::ex2(mx - top);
+          sum += c * from[x * (D + 2) + D + 1];
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[i] += c * from[x * (D + 2) + lane * E + i];
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float out = acc[i] / sum * (1.f / kSmall);
+          if (slot < 0) p.o[((int64_t)w.b * Hq + head) * D + lane * E + i] = __float2bfloat16_rn(out);
+          else p.part_o[((int64_t)slot * kDecodeGroup + own) * D + lane * E + i] = out;
+        }
+        if (lane == 0) {
+          if (slot < 0) p.lse[(int64_t)head * p.B + w.b] = 0.6931471805599453f * (top + log2f(sum));
+          else p.part_sum[(int64_t)slot * kDecodeGroup + own] = make_float2(top, sum);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
 
 template <int D, int FMT, int NB>
 __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const DecodeParams p) {
+    decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const __grid_constant__ DecodeParams p) {
   using C = DecodeCfg<D, FMT, NB>;
   constexpr bool BF = FMT == kFmtBf16;
   extern __shared__ uint8_t smem_raw[];
@@ -340,6 +504,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     ptx::mbar_init(&sm.sync, kDecodeHelpers);
     ptx::mbar_fence_init();
     sm.abort = 0;
+    sm.redo = 0;
     sm.first_rank = sm.end_rank = 0;
     sm.pair0 = sm.tile0 = 0;
     ptx::tma_prefetch_desc(&tk);
@@ -597,13 +762,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     };
     constexpr int KS = D / 16, OC = D / 4;
     const int g = lane >> 2, t = lane & 3, quarter = warp & 3;
-    auto join = [&](int k) {
+    auto join = [&](int k, uint32_t chunk) {
       const auto& mail = sm.mail[k];
       ptx::tc_fence_after();
       const int32_t b = mail.b, h0 = mail.h0, slot = mail.slot;
       // The largest unit of the warps' O. It is applied to the finished quotients: as part of a weight it would take
       // values near the smallest floats below them.
-      const int32_t vtop = BF ? 0 : __reduce_max_sync(0xffffffffu, lane < C::WARPS ? mail.vref[lane] : 0);
+      int32_t vtop = 0;
+      if (!BF) {
+        const int32_t v = lane < C::WARPS ? mail.vref[lane] : 255 << 8;
+        vtop = __reduce_max_sync(0xffffffffu, v & 255);
+        if (vtop - __reduce_min_sync(0xffffffffu, v >> 8) > kDecodeSpread && warp == C::WARPS && lane == 0)
+          sm.redo |= 1u << min(chunk, 31u);
+      }
       const float unit = BF ? 1.f : row_scale(vtop);
 #pragma unroll 1
       for (int nb = 0; nb < NB; ++nb) {
@@ -646,7 +817,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           tmem_get<OC>(tmem + k * C::MAIL_COLS + x * C::OCOLS + nb * OC, r);
           const int from = quarter + 4 * x;  // consumer warp w is on the quarter w mod 4
           const float2 mw = *reinterpret_cast<const float2*>(&mail.m[from * 8 * NB + nb * 8 + 2 * t]);
-          const float rel = BF ? 1.f : exp2_int(mail.vref[from] - vtop - 14);
+          const float rel = BF ? 1.f : exp2_int((mail.vref[from] & 255) - vtop - 14);
           const float w0 = mw.x == -INFINITY ? 0.f : ptx::ex2(mw.x - top[0]) * rel;
           const float w1 = mw.y == -INFINITY ? 0.f : ptx::ex2(mw.y - top[1]) * rel;
           ptx::tmem_ld_wait();
@@ -759,7 +930,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
                                               : ptx::mbar_try_wait(&sm.mail_full[k], parity))) {
           idle = 0;
           done = sm.mail[k].final != 0;
-          if (!join(k)) break;
+          if (!join(k, mails)) break;
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sm.mail_empty[k]);
           ++mails;
@@ -804,7 +975,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     // rounding of the scaled maximum, a factor of 2 or more from logits of 2^25 on: past the range of fp16, then of fp32.)
     float head_scale[NB][2];                     // of heads 2t, 2t + 1: what takes q' . k' to y but for the K row's exponent
     float m[NB][2], l[NB][2], o[NB][KS][4];
-    int32_t vref = 0;                            // r + 127
+    int32_t vref = 0;                            // r + 127: the largest y of the chunk so far
+    int32_t vlow = 255;                          // the smallest that this lane saw
     uint32_t mails = 0;
     int tick = 0, s = -1;
     uint32_t phase = 1;
@@ -821,6 +993,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         // ---- a chunk begins: query fragments, running values
         const uint8_t* qs = extra + C::SCALE_BYTES;
         vref = 0;
+        vlow = 255;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int head = nb * 8 + g;
@@ -916,6 +1089,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           const int32_t y = at[1 << p.log2_page];
           const bool seen = !edge || (r >= v0 && r < v1);
           const int32_t top = max(vref, __reduce_max_sync(0xffffffffu, seen && y != kRowNaN ? y : 0));
+          vlow = min(vlow, seen ? y : 255);
           // a hidden token's byte may be anything: its weight is zero whatever that says
           const float v_mine = !seen ? 0.f : y == kRowNaN ? __uint_as_float(0x7fffffffu) : exp2_int(y - top + 14);
           vshift = exp2_int(vref - top);
@@ -1076,8 +1250,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         tmem_put<D / 4>(tmem + k * C::MAIL_COLS + (warp >> 2) * C::OCOLS + nb * (D / 4),
                         reinterpret_cast<const uint32_t*>(&o[nb][0][0]));
       }
+      if (!BF) vlow = __reduce_min_sync(0xffffffffu, vlow);
       if (lane == 0) {
-        mail.vref[warp] = vref;
+        mail.vref[warp] = vref | vlow << 8;
         if (warp == 0) {
           mail.b = h.b;
           mail.h0 = h.h0;
@@ -1096,6 +1271,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   if (warp == C::WARPS) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(sm.tmem, C::TMEM_COLS);
+  }
+  if constexpr (!BF) {
+    static_assert(4 * redo_scratch<D>(C::WARPS + kDecodeHelpers) <= C::STAGES * C::STAGE_BYTES, "decode_redo's scratch");
+    if (sm.redo != 0 && !sm.abort)
+      decode_redo<D, FMT>(p, reinterpret_cast<float*>(ring), sm.pair0, sm.tile0, sm.end_rank - sm.first_rank, sm.redo,
+                          C::WARPS + kDecodeHelpers);
   }
 }
 

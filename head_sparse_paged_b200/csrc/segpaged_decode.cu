@@ -307,6 +307,8 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   p.part_sum = reinterpret_cast<float2*>(ws + align256(kMetaBytes));
   p.part_o = reinterpret_cast<float*>(ws + align256(kMetaBytes) + align256(kSlots * kDecodeGroup * sizeof(float2)));
   p.kv_scale = kv_scale;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
   p.table = page_table;
   p.offs = page_table_offs;
   p.ctx_len = ctx_len;

@@ -452,8 +452,11 @@ size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims);
  *     matter. A call owns it while it runs: calls (or replayed graphs) that may overlap on the GPU need one each.
  *   o and lse must not overlap q or one another.
  * Logits (times log2(e), rounded to fp32 once), sums and O are held in fp32 and have to stay within its range; of a bf16
- * pool q.k has to as well, of an 8-bit pool a query row times softmax_scale has to stay below 2^110. A probability is
- * rounded to fp16 (8-bit pools) or to a sum of two bf16 (bf16 pools). The result does not depend on the physical page ids.
+ * pool q.k has to as well, of an 8-bit pool a query row times softmax_scale has to stay below 2^110. Of a bf16 pool a
+ * probability is rounded to a sum of two bf16. Of an 8-bit pool a probability times its V row's 2^(y-127) is rounded to
+ * fp16: by 2^-11 of itself, or by 2^-28 of the largest such weight of its head where that is more. Where the y of the V
+ * rows that one thread block reads of a (sequence, KV head) lie more than 11 apart, weights are not rounded, and that
+ * share takes up to 15 times as long. The result does not depend on the physical page ids.
  * A sequence with L_b = 0 (an unused batch slot) gets O = 0 and LSE = -infinity. Two kernels are launched, both able to
  * start while the work before them ends (programmatic dependent launches; they wait for it before touching memory).
  */
