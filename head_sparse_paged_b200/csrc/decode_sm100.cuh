@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       nxt.id = 0;
       if (nxt.need) {  // nothing waits for the load before its batch is issued
         const int32_t lp = (int32_t)(tok >> p.log2_page);
-        nxt.id = __ldg(p.table + off + (lp < sink ? lp : lp - w0 + sink));
+        nxt.id = p.table[off + (lp < sink ? lp : lp - w0 + sink)];
       }
       return min(batch_tiles, (stop - i0 + n_step - 1) >> log2_step);
     };
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       cur.id = 0;
       if (cur.need) {
         const int32_t lp = (int32_t)(tok >> p.log2_page);
-        cur.id = __ldg(p.table + w0.off + (lp < w0.n_sink ? lp : lp - w0.w0 + w0.n_sink));
+        cur.id = p.table[w0.off + (lp < w0.n_sink ? lp : lp - w0.w0 + w0.n_sink)];
       }
       cur.h = header(0, tile, w0.g.n, sm.pair0, w0.g.n - tile, sp, lane == 0);
       cur.h.b = w0.b;

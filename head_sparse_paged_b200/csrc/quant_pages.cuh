@@ -95,7 +95,8 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c, int half, const
 }
 
 // For kernels that may be launched while the work before them still runs: waits for its end, before anything is read or
-// written, and lets the launch after this one get ready meanwhile.
+// written, and lets the launch after this one get ready meanwhile. What that work wrote is read with ordinary loads:
+// __ldg takes memory that nobody writes while the kernel runs, its wait included, and may be moved above the wait.
 __device__ __forceinline__ void early_start() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -146,10 +147,10 @@ __global__ void __launch_bounds__(32 * kSliceWarps) build_quant_kernel(BuildQuan
       const int64_t tok = tok0 + i * ROWS + lane / LANES;
       if (tok >= hp.L) continue;
       const int64_t src = ((src0 + tok) * p.Hkv + kh) * D + 8 * c;
-      k[i].lo = __ldg(reinterpret_cast<const uint4*>(p.k_dense + src));
-      k[i].hi = __ldg(reinterpret_cast<const uint4*>(p.k_dense + src + D / 2));
-      v[i].lo = __ldg(reinterpret_cast<const uint4*>(p.v_dense + src));
-      v[i].hi = __ldg(reinterpret_cast<const uint4*>(p.v_dense + src + D / 2));
+      k[i].lo = *reinterpret_cast<const uint4*>(p.k_dense + src);
+      k[i].hi = *reinterpret_cast<const uint4*>(p.k_dense + src + D / 2);
+      v[i].lo = *reinterpret_cast<const uint4*>(p.v_dense + src);
+      v[i].hi = *reinterpret_cast<const uint4*>(p.v_dense + src + D / 2);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -206,10 +207,10 @@ __global__ void __launch_bounds__(32) append_kernel(AppendParams p) {
   k.lo = k.hi = v.lo = v.hi = make_uint4(0, 0, 0, 0);
   if (ok) {  // issued before the page look-up, whose loads depend on one another
     const int64_t src = ((int64_t)r * p.Hkv + kh) * D + 8 * c;
-    k.lo = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
-    k.hi = __ldg(reinterpret_cast<const uint4*>(p.k_new + src + D / 2));
-    v.lo = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
-    v.hi = __ldg(reinterpret_cast<const uint4*>(p.v_new + src + D / 2));
+    k.lo = *reinterpret_cast<const uint4*>(p.k_new + src);
+    k.hi = *reinterpret_cast<const uint4*>(p.k_new + src + D / 2);
+    v.lo = *reinterpret_cast<const uint4*>(p.v_new + src);
+    v.hi = *reinterpret_cast<const uint4*>(p.v_new + src + D / 2);
   }
   const int32_t first = p.cu_new[0], end = p.cu_new[p.B];
   if (r < first || r >= end) return;  // rows outside every sequence are left alone (the whole warp's row)
@@ -318,10 +319,10 @@ __global__ void __launch_bounds__(32 * kSliceWarps) dequant_pages_kernel(Dequant
     int32_t ky[N], vy[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      k[i] = __ldg(reinterpret_cast<const uint2*>(p.k_pool + at + i * ROWS * D));
-      v[i] = __ldg(reinterpret_cast<const uint2*>(p.v_pool + at + i * ROWS * D));
-      ky[i] = __ldg(sc + i * ROWS);
-      vy[i] = __ldg(sc + i * ROWS + (1 << p.log2_page));
+      k[i] = *reinterpret_cast<const uint2*>(p.k_pool + at + i * ROWS * D);
+      v[i] = *reinterpret_cast<const uint2*>(p.v_pool + at + i * ROWS * D);
+      ky[i] = sc[i * ROWS];
+      vy[i] = sc[i * ROWS + (1 << p.log2_page)];
     }
     const int bk = warp_find(p.offs, nheads, e), b = bk / p.Hkv;
     const int32_t t = (int32_t)(e - p.offs[bk]);
