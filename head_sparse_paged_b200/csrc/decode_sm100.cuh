@@ -60,6 +60,13 @@ constexpr int kDecodeMails = 2;          // finished chunks that tensor memory h
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
 constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
+// Tries (of 0.2 to some 6 us) that a helper makes in a row without anything to do before it gives up: 1 to 25 s; other roles'
+// waits end after 1 s. It looks at that, and at whether another warp has given up, once in SEGPAGED_DECODE_IDLE_CHECK tries (a power of two). A test builds
+// the kernels with limits that run out.
+#ifndef SEGPAGED_DECODE_IDLE_TRIES
+#define SEGPAGED_DECODE_IDLE_TRIES (1 << 22)
+#define SEGPAGED_DECODE_IDLE_CHECK 64
+#endif
 constexpr int kDecodeSpread = 11;        // how far apart the exponent bytes of a chunk's V rows may lie in fp16 weights
 
 struct DecodeParams {
@@ -320,6 +327,7 @@ struct DecodeSmall {
   int32_t pair0, tile0;                         // where its first tile lies
   int32_t abort;
   uint32_t tmem;
+  int32_t last[8];                              // the last tile that was issued into each stage, -1 if none was
   uint32_t redo;                                // bit c: chunk c of the run is to be done again (31: and those after it)
   DecodePair window[32];                        // pairs pair0 ..
 };
@@ -505,6 +513,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     ptx::mbar_fence_init();
     sm.abort = 0;
     sm.redo = 0;
+    for (int s = 0; s < 8; ++s) sm.last[s] = -1;
     sm.first_rank = sm.end_rank = 0;
     sm.pair0 = sm.tile0 = 0;
     ptx::tma_prefetch_desc(&tk);
@@ -710,8 +719,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       }
       return min(batch_tiles, (stop - i0 + n_step - 1) >> log2_step);
     };
-    // Fills stage s with the tile whose boxes the lanes box_tile * boxes .. have in `c`.
-    auto issue = [&](int s, const Box& c, int32_t box_tile) {
+    // Fills stage s with the run's tile i, whose boxes the lanes box_tile * boxes .. have in `c`.
+    auto issue = [&](int s, int32_t i, const Box& c, int32_t box_tile) {
       uint8_t* stage = ring + s * C::STAGE_BYTES;
       uint8_t* extra = extras + s * C::EXTRA_BYTES;
       const bool load = my_tile == box_tile && c.need;
@@ -720,6 +729,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       const bool with_q = __shfl_sync(0xffffffffu, c.h.flags, leader) & 1;
       if (lane == leader) {
         sm.hdr[s] = c.h;
+        sm.last[s] = i;
         ptx::mbar_arrive_expect_tx(&sm.full[s], __popc(have) * 2 * box * D * C::EB + (with_q ? heads * D * 2 : 0));
       }
       __syncwarp();
@@ -871,7 +881,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
     };
 
     // Both jobs in turn: a copy as soon as its stage is free, a join as soon as a chunk is in the mail.
-    int32_t i = warp - C::WARPS, left = 0, at_box = 0, ahead = -1, issued = -1;  // issued: the last tile
+    int32_t i = warp - C::WARPS, left = 0, at_box = 0, ahead = -1;
     bool producing = tiles > 0 && i < n_step, done = tiles == 0;
     uint32_t mails = 0;
     int32_t idle = 0;
@@ -893,8 +903,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
       cur.h.b = w0.b;
       cur.h.h0 = w0.h0;
       check_id(cur);
-      issue(0, cur, 0);
-      issued = 0;
+      issue(0, 0, cur, 0);
       i = n_step;
       cur.need = false;
     }
@@ -916,8 +925,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
         const int s = i % C::STAGES;
         if (i < C::STAGES || __all_sync(0xffffffffu, ptx::mbar_try_wait(&sm.empty[s], ((i / C::STAGES) - 1) & 1))) {
           idle = 0;
-          issue(s, cur, at_box);
-          issued = i;
+          issue(s, i, cur, at_box);
           --left;
           ++at_box;
           i += n_step;
@@ -936,19 +944,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
           ++mails;
         }
       }
-      if ((++idle & 63) == 0) {  // a bounded wait, as ptx::mbar_wait: seconds of tries of 200 ns
-        if (idle > 1 << 24) {
+      if ((++idle & (SEGPAGED_DECODE_IDLE_CHECK - 1)) == 0) {  // a bounded wait, as ptx::mbar_wait
+        if (idle > SEGPAGED_DECODE_IDLE_TRIES) {
           sm.abort = 1;
           report(p.status, kDecodeStatusTimeout);
         }
         if (__any_sync(0xffffffffu, *(volatile int32_t*)&sm.abort != 0)) break;
       }
     }
-    // after a timeout: the copies in flight land before the block's memory is given up
-    if (*(volatile int32_t*)&sm.abort)
-#pragma unroll 1
-      for (int32_t k = issued; k >= 0 && k > issued - C::STAGES; k -= n_step)
-        ptx::mbar_wait(&sm.full[k % C::STAGES], (k / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
   } else {
     // ----------------------------------------------------------------------------------- consumers
     constexpr int KS = D / 16;  // k16 steps of a logit, and m16 tiles of O^T
@@ -1271,6 +1274,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, FMT, NB>::THREADS, 1)
   if (warp == C::WARPS) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(sm.tmem, C::TMEM_COLS);
+    // After a timeout: the copies in flight land before the block's memory is given up. Nobody issues any more, so that the
+    // last tile of a stage is the one its barrier's phase is at. (For its tile before that a parity could be one of two.)
+    if (sm.abort) {
+#pragma unroll 1
+      for (int s = 0; s < C::STAGES; ++s)
+        if (sm.last[s] >= 0)
+          ptx::mbar_wait(&sm.full[s], (sm.last[s] / C::STAGES) & 1, nullptr, p.status, kDecodeStatusTimeout);
+    }
   }
   if constexpr (!BF) {
     static_assert(4 * redo_scratch<D>(C::WARPS + kDecodeHelpers) <= C::STAGES * C::STAGE_BYTES, "decode_redo's scratch");
