@@ -349,6 +349,7 @@ class Decoder:
                                     for _ in range(2))
         self.kv_scale = None if kv == "bf16" else torch.zeros(self.dims.num_pages, 2, P, dtype=torch.uint8, device=dev)
         self.ctx_dev = torch.from_numpy(self.ctx).to(dev)
+        self.device = self.ctx_dev.device                      # with its index
         self.ql_dev = torch.from_numpy(self.ql).to(dev)
         self.cu_new = torch.arange(B + 1, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -408,9 +409,18 @@ class Decoder:
                 head.extend(self._take(int(n) - len(head)))
             self._upload_table(li)
 
+    def check_inputs(self, q, k_new, v_new):
+        """Raises ValueError for step inputs that are not what copying them into the step's buffers would keep as it is."""
+        w = self.w
+        for t, heads, name in ((q, w.num_q_heads, "q"), (k_new, w.num_kv_heads, "k_new"), (v_new, w.num_kv_heads, "v_new")):
+            shape = (w.num_seqs, heads, w.head_dim)
+            if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != self.device:
+                raise ValueError(f"{name}: expected {shape} bfloat16 on {self.device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+
     def step(self, li, q, k_new, v_new, stream=None):
         """Layer li's attention of the new tokens: q [B, Hq, D], k_new and v_new [B, Hkv, D] bf16 (RoPE included).
         Returns O [B, Hq, D] bf16 and LSE [Hq, B], buffers that the layer's next step overwrites."""
+        self.check_inputs(q, k_new, v_new)
         qb, kb, vb, o, lse = self.io[li]
         s = torch.cuda.current_stream(self.r.device) if stream is None else stream
         append, attend, graph = self._calls[li]
