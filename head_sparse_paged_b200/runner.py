@@ -419,15 +419,17 @@ class Decoder:
 
     def step(self, li, q, k_new, v_new, stream=None):
         """Layer li's attention of the new tokens: q [B, Hq, D], k_new and v_new [B, Hkv, D] bf16 (RoPE included).
-        Returns O [B, Hq, D] bf16 and LSE [Hq, B], buffers that the layer's next step overwrites."""
+        Returns O [B, Hq, D] bf16 and LSE [Hq, B], buffers that the layer's next step overwrites. With `stream`, what the
+        inputs wait for has to be ordered before it by the caller; they may be freed as soon as this returns."""
         self.check_inputs(q, k_new, v_new)
         qb, kb, vb, o, lse = self.io[li]
         s = torch.cuda.current_stream(self.r.device) if stream is None else stream
         append, attend, graph = self._calls[li]
         with torch.cuda.stream(s):
-            qb.copy_(q)
-            kb.copy_(k_new)
-            vb.copy_(v_new)
+            for to, t in ((qb, q), (kb, k_new), (vb, v_new)):
+                to.copy_(t)
+                if stream is not None:
+                    t.record_stream(s)  # its memory is not given out again before the copy has run
             if graph is not None:
                 graph.replay()
                 return o, lse
