@@ -353,7 +353,7 @@ class Decoder:
         self.ql_dev = torch.from_numpy(self.ql).to(dev)
         self.cu_new = torch.arange(B + 1, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.workspace = torch.empty(sp.segpaged_decode_workspace_bytes(self.dims), dtype=torch.uint8, device=dev)
+        self.workspaces = {}  # a layer's own (2.6 MB): steps of different layers may overlap on different streams
         self.pages, self.table_dev, self.offs_dev, self.io, self._calls = {}, {}, {}, {}, {}
         for li in r.layers:
             per = r.state[li].pages_per_head
@@ -372,11 +372,12 @@ class Decoder:
             kn, vn = torch.zeros(B, H, D, **bf), torch.zeros(B, H, D, **bf)
             lse = torch.zeros(w.num_q_heads, B, dtype=torch.float32, device=dev)
             self.io[li] = (q, kn, vn, o, lse)
+            self.workspaces[li] = torch.empty(sp.segpaged_decode_workspace_bytes(self.dims), dtype=torch.uint8, device=dev)
             seq = (self.ctx_dev, self.ql_dev, cls)
             tab = (self.table_dev[li], self.offs_dev[li])
             pools = (self.k_pool, self.v_pool, self.kv_scale)
             self._calls[li] = [sp.prepare_append(self.dims, kn, vn, self.cu_new, *seq, *tab, *pools, self.status),
-                               sp.prepare_attn_decode(self.dims, q, *pools, *tab, *seq, r.scale, o, lse, self.workspace,
+                               sp.prepare_attn_decode(self.dims, q, *pools, *tab, *seq, r.scale, o, lse, self.workspaces[li],
                                                       self.status), None]
 
     def _take(self, n):

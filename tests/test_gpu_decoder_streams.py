@@ -50,3 +50,31 @@ def test_inputs_may_be_freed_after_the_call(graphs):
     torch.cuda.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     del junk
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_layers_on_different_streams(kv):
+    """Steps of two layers issued on two streams, many times over, against the same steps one after the other."""
+    w, d = decoder(2, kv)
+    data = inputs(w, 2, 2)
+    d.advance()
+    want = []
+    for li in range(2):
+        o, lse = d.step(li, *data[li])
+        want.append((o.clone(), lse.clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for li in range(2):
+            for x in d.io[li][3:]:
+                x.fill_(9.0)
+        torch.cuda.synchronize()
+        for s in streams:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(200_000)           # both are queued before either runs
+        for li in range(2):
+            d.step(li, *data[li], stream=streams[li])
+        torch.cuda.synchronize()
+        for li in range(2):
+            assert torch.equal(d.io[li][3], want[li][0]) and torch.equal(d.io[li][4], want[li][1])
+    d.check_status()
