@@ -58,6 +58,7 @@ constexpr int kDecodeMaxWarps = 12;      // most consumer warps
 constexpr int kDecodeHelpers = 4;        // warps beside the consumers: one for each quarter of tensor memory's lanes
 constexpr int kDecodeMails = 2;          // finished chunks that tensor memory holds
 constexpr int kDecodeMaxCtas = 160;      // most CTAs a launch uses (B200 has 148 SMs)
+constexpr int kDecodeMostPairCost = 6;   // DecodeCfg's PAIR_COST at most
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
 constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
 // Tries (of 0.2 to some 6 us) that a helper makes in a row without anything to do before it gives up: 1 to 25 s; other roles'
@@ -140,6 +141,7 @@ struct DecodeCfg {
   // took 65.3, 63.4, 62.8 and 62.9 us and 64 of 0.1-0.9K 23.9, 22.8, 22.9 and 23.1 us; of 1, 2, 4 and 6 for bf16 108.8,
   // 107.0, 106.9, 107.4 us and 30.5, 25.6, 24.5, 24.7 us.
   static constexpr int PAIR_COST = FMT == kFmtBf16 ? 3 : 6;
+  static_assert(PAIR_COST <= kDecodeMostPairCost, "the host's check of sizes");
 };
 
 template <bool B>
@@ -158,7 +160,7 @@ struct DecodeTileHeader {
 // lo's page, of which [lo, L) are visible.
 struct DecodeGeom {
   int32_t L, a1, lo, n;
-  __device__ __forceinline__ int32_t n_a() const { return (a1 + kDecodeTile - 1) / kDecodeTile; }
+  __device__ __forceinline__ int32_t n_a() const { return (int32_t)(((uint32_t)a1 + kDecodeTile - 1) / kDecodeTile); }
   __device__ __forceinline__ int32_t b0(int32_t log2_page) const { return lo >> log2_page << log2_page; }
 };
 // A pair: those tiles, the outputs they go to, and the page table: entries [off, off + len), logical page lp at entry lp

@@ -29,7 +29,9 @@ int check_pools(const segpaged_dims* dims, int32_t fmt, bool allow_bf16, const v
   const int rc = check_dims(dims);
   if (rc) return rc;
   if (!is_8bit(fmt) && !(allow_bf16 && fmt == SEGPAGED_KV_BF16)) return SEGPAGED_ERR_FORMAT;
-  if ((int64_t)dims->num_seqs * dims->num_q_heads > INT32_MAX) return SEGPAGED_ERR_DIMS;
+  // the kernels index query heads, and three class values a KV head, with 32 bits
+  if ((int64_t)dims->num_seqs * dims->num_q_heads > INT32_MAX || (int64_t)dims->num_seqs * dims->num_kv_heads > INT32_MAX / 3)
+    return SEGPAGED_ERR_DIMS;
   if (dims->num_seqs == 0) return SEGPAGED_OK;
   if (!k_pool || !v_pool || (is_8bit(fmt) && !kv_scale)) return SEGPAGED_ERR_NULL;
   if (!aligned16(k_pool) || !aligned16(v_pool) || (is_8bit(fmt) && !aligned16(kv_scale))) return SEGPAGED_ERR_ALIGN;
@@ -296,6 +298,9 @@ extern "C" int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format
   if (!q || (!page_table && page_table_len > 0) || !page_table_offs || !ctx_len || !cls || !o || !lse || !workspace) return SEGPAGED_ERR_NULL;
   if (workspace_bytes < segpaged_decode_workspace_bytes(dims)) return SEGPAGED_ERR_CAPACITY;
   if (!aligned16(q) || !aligned16(o) || !aligned16(workspace)) return SEGPAGED_ERR_ALIGN;
+  // The kernel counts half tiles, and kDecodeMostPairCost for each pair, in 32 bits. Tiles are fewer than table entries.
+  const int64_t pairs = (int64_t)dims->num_seqs * dims->num_kv_heads, passes = std::max(dims->num_q_heads / dims->num_kv_heads / kDecodeGroup, 1);
+  if (page_table_len > INT32_MAX || (2 * page_table_len + kDecodeMostPairCost * pairs) * passes > UINT32_MAX) return SEGPAGED_ERR_DIMS;
   const float scale_log2 = softmax_scale * 1.4426950408889634f;
   if (!std::isfinite(scale_log2)) return SEGPAGED_ERR_DIMS;
   const int sms = sm_count();

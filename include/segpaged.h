@@ -383,7 +383,7 @@ int segpaged_select_topk(int32_t num_seqs, const float* mass, const int32_t* cu_
  *   q_len (dev, nullable = 1 everywhere) [B]: the Lq_b of the storage rule that the page tables follow. It
  *     need not be the number of tokens the call works on: tables laid out for a prefill of Lq queries at
  *     length L stay valid, growing only at the end, while L and Lq are both counted up per decoded token;
- *   cls (dev) [B*Hkv]: sink < 0 counts as 0, window < 1 as 1;
+ *   cls (dev) [B*Hkv]: sink < 0 counts as 0, window < 1 as 1; B*Hkv <= (2^31 - 1) / 3 (SEGPAGED_ERR_DIMS otherwise);
  *   page_table (dev, int32) [page_table_len] (NULL only when that is 0), page_table_offs (dev, int32)
  *     [B*Hkv+1], as everywhere.
  *     A head whose table length disagrees with the storage rule sets SEGPAGED_STATUS_TABLE; a page id outside
@@ -451,6 +451,7 @@ size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims);
  *   workspace (dev) >= segpaged_decode_workspace_bytes(dims), 16-byte aligned; its contents before the call do not
  *     matter. A call owns it while it runs: calls (or replayed graphs) that may overlap on the GPU need one each.
  *   o and lse must not overlap q or one another.
+ *   page_table_len < 2^31 and (2 page_table_len + 6 B*Hkv) max(1, Hq/Hkv/16) < 2^32 (SEGPAGED_ERR_DIMS otherwise).
  * Logits (times log2(e), rounded to fp32 once), sums and O are held in fp32 and have to stay within its range; of a bf16
  * pool q.k has to as well, of an 8-bit pool a query row times softmax_scale has to stay below 2^110. Of a bf16 pool a
  * probability is rounded to a sum of two bf16. Of an 8-bit pool a probability times its V row's 2^(y-127) is rounded to

@@ -189,3 +189,16 @@ def test_binding_refuses_mismatched_tensors(monkeypatch):
         sp.prepare_pages_dequant(dims, good["ctx_len"], None, good["cls"], good["page_table"], good["page_table_offs"],
                                  good["k_pool"], good["v_pool"], good["kv_scale"], _Fake((9, 16, 64), bf),
                                  _Fake((10, 16, 64), bf))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_more_heads_than_the_kernels_can_index_are_refused(name):
+    """(sequence, KV head) pairs are counted in 32 bits, three class values each."""
+    assert _call(name, sp.Dims(400_000_000, 2, 2, 64, 16, 10)) == DIMS
+
+
+def test_more_tiles_than_the_attention_can_count_are_refused():
+    """Half tiles of all passes over the tables, and six for the end of each pair, are counted in 32 bits."""
+    for dims, tlen in ((sp.Dims(1, 8, 8, 64, 16, 10), 1 << 31), (sp.Dims(1, 8, 8, 64, 16, 10), 1 << 40),
+                       (sp.Dims(1, 128, 1, 64, 16, 10), 1 << 28), (sp.Dims(700_000_000, 1, 1, 64, 16, 10), 1 << 28)):
+        assert _call("segpaged_attn_decode", dims, tlen=tlen) == DIMS, (dims, tlen)
