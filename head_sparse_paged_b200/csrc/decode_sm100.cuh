@@ -3,15 +3,17 @@
 // For sequence b, KV head k and the G query heads h of its group, at position i = L - 1:
 //   s_j = scale q_h . k_j over the visible keys j,  O_h = sum_j softmax(s)_j v_j,  LSE_h = ln sum_j exp(s_j).
 // Every visible key and value is read once and used by G heads only, so the call is bound by HBM (for G = 8, 16
-// flops per bf16 byte, where mma.sync passes about 60). What matters is that all SMs load all the time. So:
+// flops per bf16 byte, where mma.sync passes about 60). (A group of more than 16 heads is done in passes of 16, each of which
+// reads and converts the tiles again: 32 sequences of 16-32K take 79, 143, 272 and 521 us in e4m3 and 112, 208, 404 and 789
+// us in bf16 with 16, 32, 64 and 128 heads a KV head.) What matters is that all SMs load all the time. So:
 //   - The work is the list of 128-token tiles of all (sequence, KV head) pairs, cut into one equal run of tiles per
 //     CTA (one CTA per SM): a pair's tiles may end in one CTA and go on in the next. Each CTA finds its run by itself
-//     from ctx_len and the classes in device memory (a prefix sum over the pairs, 1.5-2 us), so a captured call follows the
+//     from ctx_len and the classes in device memory (a prefix sum over the pairs), so a captured call follows the
 //     lengths and there is no host plan. Runs that end inside a pair leave a partial result (O / l, m and l) in
 //     the workspace, which decode_combine_kernel joins in tile order: no atomics, no state from call to call, and the
-//     result depends on the lengths and the grid only.
+//     rounding depends on the lengths, the size of the table array (see kDecodeWholeTokens) and the grid only.
 //   - Two to four helper warps stream the tiles through a ring of shared-memory stages with TMA (page id = coordinate),
-//     three (bf16) or six (8-bit) tiles deep, across pair boundaries, with the page ids of the next tiles in flight.
+//     three to eight tiles deep (as many as fit, see DecodeCfg), across pair boundaries, with the next page ids in flight.
 //   - Eight or twelve consumer warps take 32 tokens of every second or third tile, and keep their own
 //     running maximum, sum and O in registers. S^T = K Q^T puts the tokens on the 16 rows of mma.m16n8k16 and the heads
 //     on its 8 columns, so up to 8 heads cost the same and nothing is padded from 8 to 16; O^T = V^T P^T likewise.
@@ -35,7 +37,7 @@
 // costs a second V product where the tensor pipe idles.
 //
 // Measured (B200, back-to-back calls; of the 6543 GB/s that a large copy reaches): 32 sequences of 16-32K, 64/8 heads,
-// one global head each: bf16 106.4 us, 6.2 TB/s (94 %); e4m3 62.0 us, 5.3 TB/s (82 %); int8 64.2 us. 64 global heads at
+// one global head each: bf16 106.7 us, 6.2 TB/s (94 %); e4m3 61.9 us, 5.3 TB/s (82 %); int8 63.8 us. 64 global heads at
 // 128K: bf16 614 us, 7.0 TB/s (107 %); e4m3 321 us, 6.7 TB/s (103 %), 337 us after seconds of it, when the power cap
 // holds the SMs at 1.6 GHz and the conversions' ALU work (53 % of its pipe at 1.9 GHz) no longer hides. What the short
 // calls are made of, on 32 sequences in e4m3: 2.6 us to find the run, 1.2 us to issue the first copies, 1.4 us to the first
@@ -137,9 +139,10 @@ struct DecodeCfg {
   static constexpr int TMEM_COLS = kDecodeMails * MAIL_COLS <= 64 ? 64 : kDecodeMails * MAIL_COLS <= 128 ? 128 : 256;
   static_assert(kDecodeMails * MAIL_COLS <= TMEM_COLS, "tensor memory");
   static_assert(MAIL <= 192 && WARPS % 4 == 0 && WARPS <= kDecodeMaxWarps, "a mail's arrays, the quarters");
-  // What ending a pair costs a CTA, in half tiles of 128 columns. Of 3, 5, 7 and 9 for 8-bit pools 32 sequences of 16-32K
-  // took 65.3, 63.4, 62.8 and 62.9 us and 64 of 0.1-0.9K 23.9, 22.8, 22.9 and 23.1 us; of 1, 2, 4 and 6 for bf16 108.8,
-  // 107.0, 106.9, 107.4 us and 30.5, 25.6, 24.5, 24.7 us.
+  // What ending a pair costs a CTA, in half tiles. With 3, 5, 6, 7 and 9 for 8-bit pools 32 sequences of 16-32K in e4m3 take
+  // 63.5, 62.1, 61.6, 62.1 and 62.3 us and 64 of 0.1-0.9K 22.2, 21.8, 21.8, 22.1 and 22.3 us (D = 128); with 64 columns 44.9,
+  // 45.0, 45.4, 45.7, 46.5 and 17.0, 16.4, 16.4, 16.7, 16.7 us. With 1, 2, 3, 4 and 6 for bf16 107.1, 106.6, 106.7, 106.3,
+  // 106.6 and 30.6, 25.1, 24.5, 24.2, 24.5 us; with 64 columns 60.5, 60.5, 60.4, 60.3, 60.8 and 18.6, 18.4, 17.6, 17.4, 17.3.
   static constexpr int PAIR_COST = FMT == kFmtBf16 ? 3 : 6;
   static_assert(PAIR_COST <= kDecodeMostPairCost, "the host's check of sizes");
 };

@@ -3,10 +3,10 @@
 // All three move each byte once and are bound by HBM: 2 bytes read and 1 written per element (the write), or the
 // reverse (the read back). A warp takes 8 rows of a page and issues all their loads before it uses the first: 4 KB (2 KB
 // for the read back) in flight a warp, in slices small enough to spread evenly over the GPU. On a batch of four 16-32K
-// contexts (126 MB) that takes 25.1 us for the write and 25.0 us for the read back, 5.0 TB/s, where a plain copy of as
-// many bytes takes 23.4 us; slices of 16 rows took 26.8 and 25.0 us. A whole page per block, found by a binary search,
-// took 30.7 us both ways: 2.5 us of dependent loads before each page's data, and blocks with three pages beside blocks
-// with two.
+// contexts (126 MB) that takes 23.2 us for the write and 22.8 us for the read back, 5.4 and 5.5 TB/s, where a plain copy of
+// as many bytes takes 23.4 us. (Without the early start of the launches 25.1 and 25.0 us, against 26.8 and 25.0 us with
+// slices of 16 rows, and 30.7 us both ways with a whole page per block, found by a binary search: 2.5 us of dependent loads
+// before each page's data, and blocks with three pages beside blocks with two.)
 // In the kernels that quantise, lane c of a row holds its elements 8c .. 8c+7 and D/2 + 8c .. D/2 + 8c+7, the pairs that
 // the RoPE re-alignment rotates, so that the row's largest magnitude is taken of the rotated bf16 values: a pool written
 // here holds the quantised form of exactly the rows that build_scatter_kernel would store.

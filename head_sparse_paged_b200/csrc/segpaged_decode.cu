@@ -104,7 +104,7 @@ bool encode_pool(CUtensorMap* map, const void* base, int P, int64_t pages) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Where all the tables together hold no more tokens than this, no (sequence, KV head) is cut into chunks and nothing is left
+// Where the table array has room for no more tokens than this (page_table_len is all the host knows of the tables), no (sequence, KV head) is cut into chunks and nothing is left
 // to join: even if they are all one pair's, its tiles one after the other take no longer than the second launch. One head
 // of 256, 512, 640, 768 tokens (D = 128, e4m3, replayed graphs): 8.1, 9.3, 9.8, 10.3 us whole, 9.9, 10.0, 10.1, 10.0 us
 // cut and joined; eight heads of 64: 7.4 against 9.0 us. bf16 and D = 64 cross at or above 640 too.

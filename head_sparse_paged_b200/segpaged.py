@@ -540,7 +540,8 @@ def prepare_pages_dequant(dims: Dims, ctx_len, q_len, cls, page_table, page_tabl
 
 def segpaged_pages_dequant(dims: Dims, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool, kv_scale, k_out,
                            v_out, status=None, stream=None):
-    """Every stored page of 8-bit pools read back into bf16 pools of the same page ids."""
+    """Every stored page of 8-bit pools read back into bf16 pools of the same page ids; rows past a context's end are zero
+    (undefined where tables of different lengths share the page)."""
     prepare_pages_dequant(dims, ctx_len, q_len, cls, page_table, page_table_offs, k_pool, v_pool, kv_scale, k_out, v_out,
                           status)(stream)
 

@@ -380,7 +380,9 @@ int segpaged_select_topk(int32_t num_seqs, const float* mass, const int32_t* cu_
  * Lengths and classes are read from device memory, and nothing is planned on the host, so a captured
  * call can be replayed while the lengths, tables and classes in those arrays change. In all calls below
  *   ctx_len (dev) [B]: L_b, the new tokens included (a negative value counts as 0);
- *   q_len (dev, nullable = 1 everywhere) [B]: the Lq_b of the storage rule that the page tables follow. It
+ *   q_len (dev, nullable = 1 everywhere; segpaged_build_quant needs it) [B]: the Lq_b of the storage rule that
+ *     the page tables follow. Below 0 it counts as 0, and for segpaged_attn_decode, whose token is a query,
+ *     below 1 as 1: of a table laid out for no query at all it may miss a page (SEGPAGED_STATUS_TABLE). It
  *     need not be the number of tokens the call works on: tables laid out for a prefill of Lq queries at
  *     length L stay valid, growing only at the end, while L and Lq are both counted up per decoded token;
  *   cls (dev) [B*Hkv]: sink < 0 counts as 0, window < 1 as 1; B*Hkv <= (2^31 - 1) / 3 (SEGPAGED_ERR_DIMS otherwise);
@@ -389,6 +391,8 @@ int segpaged_select_topk(int32_t num_seqs, const float* mass, const int32_t* cu_
  *     A head whose table length disagrees with the storage rule sets SEGPAGED_STATUS_TABLE; a page id outside
  *     [0, num_pages) sets SEGPAGED_STATUS_PAGE_ID. All accesses stay in bounds; what is computed for such a
  *     head is undefined.
+ * Tables may name the same page (a shared prefix). The attention reads it from each. Calls that write go over
+ * it once for every table that names it, in no order, so that all of them have to give it the same contents.
  *
  * 8-bit pools. k_pool and v_pool are [num_pages, P, D] bytes of codes, and kv_scale (16-byte aligned) is
  * [num_pages, 2, P] exponent bytes, the K rows' before the V rows'. A row (the D values of one token and KV
@@ -429,7 +433,8 @@ int segpaged_append(const segpaged_dims* dims, int32_t kv_format, const void* k_
 /*
  * Reads every stored page of 8-bit pools back into bf16 pools k_out, v_out (dev) [num_pages, P, D] at the same
  * physical ids (one kernel launch), as the prefill-side calls take them: c * 2^(y-127) rounded to nearest even,
- * which only rounds below the bf16 normal range. Rows past L_b are written as zero. Pages not named by any
+ * which only rounds below the bf16 normal range. Rows past L_b are written as zero, so of a page that tables
+ * of different lengths share the rows past the shortest are undefined. Pages not named by any
  * table are not touched. Returns SEGPAGED_ERR_FORMAT for SEGPAGED_KV_BF16. k_out and v_out must not overlap the
  * 8-bit pools.
  */
@@ -458,8 +463,9 @@ size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims);
  * fp16: by 2^-11 of itself, or by 2^-28 of the largest such weight of its head where that is more. Where the y of the V
  * rows that one thread block reads of a (sequence, KV head) lie more than 11 apart, weights are not rounded, and that
  * share takes up to 15 times as long. The result does not depend on the physical page ids.
- * A sequence with L_b = 0 (an unused batch slot) gets O = 0 and LSE = -infinity. Two kernels are launched, both able to
- * start while the work before them ends (programmatic dependent launches; they wait for it before touching memory).
+ * A sequence with L_b = 0 (an unused batch slot) gets O = 0 and LSE = -infinity. Two kernels are launched, or one where
+ * page_table_len pages hold no more than 640 tokens, able to start while the work before them ends (programmatic
+ * dependent launches; they wait for it before touching memory).
  */
 int segpaged_attn_decode(const segpaged_dims* dims, int32_t kv_format, const void* q, const void* k_pool,
                          const void* v_pool, const uint8_t* kv_scale, const int32_t* page_table,
