@@ -458,7 +458,8 @@ size_t segpaged_decode_workspace_bytes(const segpaged_dims* dims);
  *   o and lse must not overlap q or one another.
  *   page_table_len < 2^31 and (2 page_table_len + 6 B*Hkv) max(1, Hq/Hkv/16) < 2^32 (SEGPAGED_ERR_DIMS otherwise).
  * Logits (times log2(e), rounded to fp32 once), sums and O are held in fp32 and have to stay within its range; of a bf16
- * pool q.k has to as well, of an 8-bit pool a query row times softmax_scale has to stay below 2^110. Of a bf16 pool a
+ * pool q.k has to as well, of an 8-bit pool a query row times softmax_scale has to stay below 2^110 (below 2^-100 its
+ * logits lose precision). Of a bf16 pool a
  * probability is rounded to a sum of two bf16. Of an 8-bit pool a probability times its V row's 2^(y-127) is rounded to
  * fp16: by 2^-11 of itself, or by 2^-28 of the largest such weight of its head where that is more. Where the y of the V
  * rows that one thread block reads of a (sequence, KV head) lie more than 11 apart, weights are not rounded, and that
