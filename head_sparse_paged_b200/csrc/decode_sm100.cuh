@@ -64,8 +64,8 @@ constexpr int kDecodeMostPairCost = 6;   // DecodeCfg's PAIR_COST at most
 constexpr int kDecodeGroup = 16;         // most query heads of one pass; larger groups take several
 constexpr int kDecodeStatusTimeout = 4;  // SEGPAGED_STATUS_TIMEOUT
 // Tries (of 0.2 to some 6 us) that a helper makes in a row without anything to do before it gives up: 1 to 25 s; other roles'
-// waits end after 1 s. It looks at that, and at whether another warp has given up, once in SEGPAGED_DECODE_IDLE_CHECK tries (a power of two). A test builds
-// the kernels with limits that run out.
+// waits end after 1 s. It looks at that, and at whether another warp has given up, once in SEGPAGED_DECODE_IDLE_CHECK tries
+// (a power of two). A test builds the kernels with limits that run out.
 #ifndef SEGPAGED_DECODE_IDLE_TRIES
 #define SEGPAGED_DECODE_IDLE_TRIES (1 << 22)
 #define SEGPAGED_DECODE_IDLE_CHECK 64
